@@ -371,6 +371,157 @@ moe_status moe_inv_rope_fp8_quant_per_head(const void* x, int64_t x_token_stride
 #define MOE_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 moe_status moe_fused_forward_noalloc(const moe_fused_args* args, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The attention side of a layer around its cache.  Heads are bfloat16 rows
+ * of D values; the heads of a token are contiguous and tokens are
+ * *_token_stride elements apart (>= heads * D, a multiple of 8), so the query,
+ * key and value parts of a fused projection are taken as they lie.  Sequences
+ * are packed behind each other: cu_seqlens [B + 1] int32 holds where each
+ * starts, and the end of the last.  Offsets and lengths are read on the device
+ * and brought into the range of the tensors, so none of them leads to an
+ * access outside; rows behind the last sequence are left as they were.
+ * Sums, softmax statistics and norms are float32, outputs are rounded once.
+ * Non-finite inputs reach the outputs that depend on them, and no others.
+ * --------------------------------------------------------------------- */
+
+/*
+ * RMS norm of every query and key head and its rotary embedding, in one pass:
+ * the forward of the rotation that moe_inv_rope_fp8_quant_per_head undoes,
+ * with the same table, pair layouts and clamped positions.
+ * For token t, p = positions[t], each head x with its side's weight w:
+ *   z = x * w / sqrt(mean(x^2) + eps)      (z = x where the weight is NULL)
+ *   y1 = z1 * c - z2 * s,  y2 = z2 * c + z1 * s    (rotation by +theta)
+ * over the pairs (i, i + R/2) (interleaved == 0) or (2i, 2i + 1), features
+ * R..D-1 passing through as z; float32 throughout, rounded once.
+ *
+ *   q, k       [T][NHq][D], [T][NHk][D] bfloat16, 16-byte aligned; NHk may be
+ *              0 (k, k_weight, k_out unused)
+ *   positions, cos_sin   as in moe_inv_rope_fp8_quant_per_head
+ *   q_weight, k_weight   [D] bfloat16, or float32 with weights_f32; NULL: no
+ *              norm of that side; 16-byte aligned
+ *   q_out, k_out   as q, k (out); may be q, k themselves, and must not
+ *              overlap them otherwise
+ * Supported: D % 8 == 0 and D <= 512; R even, 0 < R <= D, R % 16 == 0
+ * (R % 8 == 0 when interleaved); eps >= 0 and finite.
+ */
+moe_status moe_qk_norm_rope(const void* q, int64_t q_token_stride, const void* k,
+                            int64_t k_token_stride, const int64_t* positions,
+                            const float* cos_sin, int64_t max_pos, int64_t T, int32_t NHq,
+                            int32_t NHk, int32_t D, int32_t R, int32_t interleaved,
+                            const void* q_weight, const void* k_weight, int32_t weights_f32,
+                            float eps, void* q_out, int64_t q_out_token_stride, void* k_out,
+                            int64_t k_out_token_stride, hipStream_t stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  A group of 32 consecutive
+ * features of one token's head shares a power of two 2^e, held as the byte
+ * e + 127; each feature is an E2M1 code (bit 3 the sign; 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6) times 2^e:
+ *   e    = the smallest with amax <= 7 * 2^e, brought into [-125, 125]
+ *   code = E2M1(x / 2^e), nearest, ties to the even code, saturating at 6
+ * 4.25 bits a value; a value read back (code * 2^e) is exact in bfloat16.  A
+ * group that holds an infinity or a NaN gets the byte 255 and reads as NaN.
+ *
+ *   pages   num_pages * moe_cache4_page_bytes(...) bytes, 16-byte aligned:
+ *           [page][NKV][page_size / 16] tiles of 16 tokens, 17 * D bytes each:
+ *             K codes  [16 tokens][D / 2]    (feature 2i: low half of byte i)
+ *             K scales [16 tokens][D / 32]
+ *             V codes  for each 128 features f: [4 quads of tokens][16 n]
+ *                      [4 tokens][4 bytes], features f + 8n .. f + 8n + 7; for
+ *                      a last 64: [4][16 n][4][2], features f + 4n .. f + 4n + 3
+ *             V scales [4 quads][D / 32][4 tokens]
+ *           (the order in which moe_cache4_attend's matrix operands take them)
+ * Supported: D 64, 128, 192 or 256; page_size a multiple of 16, at most 4096;
+ * NKV <= 65535; num_pages < 2^31.
+ */
+typedef struct {
+  void* pages;
+  int64_t num_pages;
+  int32_t page_size, NKV, D;
+} moe_cache4;
+
+/* Bytes of one page; 0 when the shape is not supported. */
+size_t moe_cache4_page_bytes(int32_t page_size, int32_t NKV, int32_t D);
+
+/*
+ * Quantises the keys and values of packed tokens into the cache.  Token
+ * cu_seqlens[b] + i goes to position start[b] + i of sequence b; position p
+ * lies in page block_table[b][p / page_size].
+ *   k, v         [T][NKV][D] bfloat16, 16-byte aligned
+ *   block_table  [B][max_pages] int32, rows table_stride apart
+ *   start        [B] int32
+ *   cu_seqlens   [B + 1] int32, or NULL: one token per sequence (T == B)
+ * A token is skipped if its position is negative or behind max_pages pages, or
+ * if its page id is not in [0, num_pages): padded sequences of a captured
+ * batch take a start of -1.  Positions of two sequences that share a page must
+ * differ (as must any two tokens' places), or the place holds a mixture.
+ */
+moe_status moe_cache4_write(const moe_cache4* cache, const void* k, int64_t k_token_stride,
+                            const void* v, int64_t v_token_stride, const int32_t* block_table,
+                            int64_t table_stride, int32_t max_pages, const int32_t* start,
+                            const int32_t* cu_seqlens, int32_t B, int64_t T, hipStream_t stream);
+
+/*
+ * Reads such tokens back as bfloat16 k, v [T][NKV][D] (out); places that
+ * moe_cache4_write would skip read as zeros.  zero_tail != 0 also zeroes the
+ * rows behind the last sequence.
+ */
+moe_status moe_cache4_read(const moe_cache4* cache, void* k, int64_t k_token_stride, void* v,
+                           int64_t v_token_stride, const int32_t* block_table,
+                           int64_t table_stride, int32_t max_pages, const int32_t* start,
+                           const int32_t* cu_seqlens, int32_t B, int64_t T, int32_t zero_tail,
+                           hipStream_t stream);
+
+/*
+ * Attention of one query token per sequence over the cache.  Query head h
+ * reads kv head h / (NHq / NKV):
+ *   s_t = scale * q . k_t,  out = sum_t softmax(s)_t v_t,
+ *   lse = log sum_t exp(s_t),   t < lens[b]
+ * lens[b] is brought into [0, max_pages * page_size]; tokens whose page id is
+ * not in [0, num_pages) are passed over; a sequence without a token gives
+ * out = 0 and lse = -inf.
+ *   q          [B][NHq][D] bfloat16, 16-byte aligned
+ *   lens       [B] int32
+ *   out        [B][NHq][D] bfloat16 (out), 16-byte aligned
+ *   lse        [B][NHq] float32 (out), or NULL
+ *   workspace  >= moe_cache4_attend_workspace_bytes(...) device bytes, 16-byte
+ *              aligned; NULL where that is 0.  Calls that may overlap, graphs
+ *              included, need workspaces of their own.
+ * Supported: NHq a multiple of NKV; B <= 65535; scale positive and finite;
+ * max_pages * page_size <= 2^28.
+ */
+size_t moe_cache4_attend_workspace_bytes(const moe_cache4* cache, int32_t B, int32_t NHq,
+                                         int32_t max_pages);
+moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_token_stride,
+                             const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                             const int32_t* lens, int32_t B, int32_t NHq, float scale, void* out,
+                             int64_t out_token_stride, float* lse, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Attention of packed prompts.  Query i of a sequence of nq queries and nk
+ * keys sees the keys j < nk, or with causal != 0 the keys
+ * j < clamp(i + 1 + nk - nq, 0, nk): the last query sees the last key, so a
+ * chunk of new queries attends to the keys before it as well.  Formulas as
+ * moe_cache4_attend; a query that sees nothing gives out = 0, lse = -inf.
+ *   q             [Tq][NHq][D] bfloat16, 16-byte aligned
+ *   k, v          [Tk][NKV][D] bfloat16, 16-byte aligned
+ *   cu_seqlens_q, cu_seqlens_k   [B + 1] int32
+ *   out           [Tq][NHq][D] bfloat16 (out), 16-byte aligned
+ *   lse           [Tq][NHq] float32 (out), or NULL
+ *   zero_tail     bit 0: rows of out behind the last sequence become 0, bit 1:
+ *                 rows of lse behind it become -inf
+ * Supported: D 64, 128, 192 or 256; NHq a multiple of NKV; scale positive and
+ * finite; Tq, Tk < 2^31 - 2^16; (Tq / 32 + B) * NHq < 2^31.
+ */
+moe_status moe_prompt_attention(const void* q, int64_t q_token_stride, const void* k,
+                                int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                int32_t B, int64_t Tq, int64_t Tk, int32_t NHq, int32_t NKV,
+                                int32_t D, int32_t causal, float scale, void* out,
+                                int64_t out_token_stride, float* lse, int32_t zero_tail,
+                                hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,6 +9,7 @@ ahead-of-time build (``build``) and the seeded synthetic workloads
 from .binding import (  # noqa: F401
     FusedLayout,
     FusedMoE,
+    KVCache4,
     NO_SECTION,
     WorkspacePool,
     MoEError,
@@ -21,5 +22,7 @@ from .binding import (  # noqa: F401
     fused_forward_noalloc,
     inv_rope_fp8_quant_per_head,
     lib,
+    prompt_attention,
+    qk_norm_rope,
     route_topk,
 )

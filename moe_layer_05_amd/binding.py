@@ -55,6 +55,17 @@ class FusedArgs(ctypes.Structure):
     ]
 
 
+class Cache4(ctypes.Structure):
+    """moe_cache4."""
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("NKV", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+    ]
+
+
 NO_SECTION = ctypes.c_size_t(-1).value
 
 
@@ -122,6 +133,34 @@ _SIGS = {
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
         ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_qk_norm_rope": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_int64, ctypes.c_void_p]),
+    "moe_cache4_page_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "moe_cache4_write": (ctypes.c_int, [
+        ctypes.POINTER(Cache4), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
+    "moe_cache4_read": (ctypes.c_int, [
+        ctypes.POINTER(Cache4), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+        ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
+    "moe_cache4_attend_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.POINTER(Cache4), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
+    "moe_cache4_attend": (ctypes.c_int, [
+        ctypes.POINTER(Cache4), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_void_p]),
+    "moe_prompt_attention": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+        ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
+        ctypes.c_void_p]),
 }
 
 # Stage boundaries of moe_fused_forward_timed (moe_stage in include/moe.h).
@@ -274,6 +313,304 @@ def inv_rope_fp8_quant_per_head(x, positions, cos_sin, R, interleaved=False, fmt
         int(bool(interleaved)), _FP8_WDTYPE[fmt], _ptr(codes), _ptr(scales), _stream(stream)),
         "moe_inv_rope_fp8_quant_per_head")
     return codes, scales
+
+
+def _heads(t, name, device=None, shape=None):
+    """The token stride of bfloat16 heads [T, heads, D] (token rows may be
+    strided, the heads of a token contiguous) on ``device``."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 CUDA (HIP) tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, D]")
+    T, H, D = t.shape
+    if shape is not None and (T, H, D) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {[T, H, D]}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    sT, sH, sD = t.stride()
+    if D > 1 and sD != 1 or H > 1 and sH != D:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return sT if T > 1 else H * D
+
+
+def _vector(t, dtype, n, name, device):
+    """The pointer of a contiguous [n] tensor on ``device``."""
+    p = _dev(t, dtype, name)
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name} must be [{n}]")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return p
+
+
+class _Launch:
+    """The stream of a call and, while entered, its device and stream as
+    torch's current ones: outputs and scratch made inside belong to that
+    stream, and inputs made on another stream are kept from reuse until the
+    call's work is done."""
+
+    def __init__(self, device, stream, inputs):
+        current = torch.cuda.current_stream(device)
+        self.other = stream is not None and stream != current
+        if self.other and stream.device != device:
+            raise ValueError(f"stream must be on {device}, got one on {stream.device}")
+        self.stream = stream if self.other else current
+        self.inputs = inputs
+        self.scope = None
+        if self.other or torch.cuda.current_device() != device.index:
+            self.scope = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.scope is not None:
+            self.scope.__enter__()
+            if self.other:
+                for t in self.inputs:
+                    if t is not None:
+                        t.record_stream(self.stream)
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *a):
+        if self.scope is not None:
+            self.scope.__exit__(*a)
+
+
+def _no_overlap(out, inputs, name):
+    """Refuses an output whose memory meets an input's."""
+    def span(t):
+        if t.numel() == 0:
+            return 0, 0
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    a0, a1 = span(out)
+    for t in inputs:
+        b0, b1 = span(t)
+        if a0 < b1 and b0 < a1:
+            raise ValueError(f"{name} must not overlap an input")
+
+
+def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out) like bfloat16 query heads q [T, NHq, D] and key heads
+    k [T, NHk, D] (or None): each head's RMS norm times its side's weight [D]
+    (bfloat16 or float32; None: no norm) and its rotary embedding at int64
+    ``positions`` [T] with the float32 table ``cos_sin`` [max_pos, R], in one
+    pass (moe_qk_norm_rope).  Token rows may be strided; ``q_out`` and
+    ``k_out`` may be q and k themselves."""
+    qs = _heads(q, "q")
+    T, NHq, D = q.shape
+    dev = q.device
+    NHk, ks = 0, 0
+    if k is not None:
+        ks = _heads(k, "k", dev)
+        NHk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k must be [{T}, heads, {D}]")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out go with k")
+    pp = _vector(positions, torch.int64, T, "positions", dev)
+    cp = _dev(cos_sin, torch.float32, "cos_sin")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != R or cos_sin.device != dev:
+        raise ValueError(f"cos_sin must be [max_pos, {R}] on {dev}")
+    wt = [w for w in (q_weight, k_weight) if w is not None]
+    f32 = bool(wt) and wt[0].dtype == torch.float32
+    for w in wt:
+        _vector(w, torch.float32 if f32 else torch.bfloat16, D, "weights", dev)
+    with _Launch(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out)) as st:
+        outs = []
+        for x, y, n in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+            if x is None:
+                outs.append((None, 0))
+                continue
+            if y is None:
+                y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+                outs.append((y, y.stride(0)))
+            else:
+                ys = _heads(y, n, dev, tuple(x.shape))
+                same = y.data_ptr() == x.data_ptr() and y.stride() == x.stride()
+                if not same:
+                    _no_overlap(y, [x], n)
+                outs.append((y, ys))
+        (qo, qos), (ko, kos) = outs
+        _check(lib().moe_qk_norm_rope(
+            q.data_ptr(), qs, _ptr(k), ks, pp, cp, cos_sin.shape[0], T, NHq, NHk, D, R,
+            int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), int(f32), eps,
+            qo.data_ptr(), qos, _ptr(ko), kos, st), "moe_qk_norm_rope")
+    return qo, ko
+
+
+class KVCache4:
+    """A paged cache of keys and values in 4 bits (E2M1 codes, a power of two
+    for every 32 features; the layout is that of moe_cache4 in include/moe.h).
+
+    ``pages`` uint8 [num_pages, NKV, page_size / 16, 17 * D] holds
+    ``num_pages`` pages of ``page_size`` tokens (a multiple of 16) for NKV
+    heads of D = 64, 128, 192 or 256 features.  Which pages a sequence has is
+    the caller's: ``block_table`` int32 [B, max_pages] names, for position p of
+    sequence b, the page block_table[b, p // page_size]; entries outside
+    [0, num_pages) hold no tokens.  The cache keeps no other state, so calls
+    may run on any stream that is ordered after the writes they read."""
+
+    def __init__(self, num_pages, page_size, NKV, D, device="cuda"):
+        nbytes = int(lib().moe_cache4_page_bytes(page_size, NKV, D))
+        if nbytes == 0:
+            raise MoEError(3, "moe_cache4_page_bytes")
+        if num_pages <= 0:
+            raise MoEError(2, "KVCache4")
+        self._bind(torch.zeros(num_pages, NKV, page_size // 16, 17 * D, dtype=torch.uint8,
+                               device=device))
+
+    @classmethod
+    def of(cls, pages):
+        """The cache held in an existing tensor of pages."""
+        self = cls.__new__(cls)
+        self._bind(pages)
+        return self
+
+    def _bind(self, pages):
+        p = _dev(pages, torch.uint8, "pages")
+        if pages.dim() != 4 or pages.shape[3] % 17:
+            raise ValueError("pages must be [num_pages, NKV, page_size / 16, 17 * D]")
+        self.pages = pages
+        self.num_pages, self.NKV, tiles, row = pages.shape
+        self.page_size, self.D = 16 * tiles, row // 17
+        self._c = Cache4(p, self.num_pages, self.page_size, self.NKV, self.D)
+
+    def _table(self, block_table, B):
+        t = block_table
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+            raise TypeError("block_table must be an int32 CUDA (HIP) tensor")
+        if t.device != self.pages.device:
+            raise ValueError(f"block_table must be on {self.pages.device}")
+        if t.dim() != 2 or t.shape[0] != B or t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"block_table must be [{B}, max_pages], its rows contiguous")
+        return t.data_ptr(), max(t.stride(0), t.shape[1]) if B > 1 else t.shape[1], t.shape[1]
+
+    def _places(self, block_table, start, cu_seqlens, T):
+        dev = self.pages.device
+        if start.dim() != 1:
+            raise ValueError("start must be [B]")
+        B = start.shape[0]
+        sp = _vector(start, torch.int32, B, "start", dev)
+        if cu_seqlens is None:
+            if T != B:
+                raise ValueError(f"{T} tokens for {B} sequences need cu_seqlens")
+            cu = None
+        else:
+            cu = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
+        return (*self._table(block_table, B), sp, cu, B, T)
+
+    def write(self, k, v, block_table, start, cu_seqlens=None, stream=None):
+        """Quantises bfloat16 keys and values [T, NKV, D] of packed sequences
+        into the cache: token i of sequence b (token cu_seqlens[b] + i; one
+        token per sequence where cu_seqlens is None) goes to position
+        start[b] + i.  Tokens without a place (a negative position, a position
+        behind the table, a page id outside the cache) are skipped."""
+        dev = self.pages.device
+        ks = _heads(k, "k", dev)
+        shape = (k.shape[0], self.NKV, self.D)
+        if tuple(k.shape) != shape:
+            raise ValueError(f"k must be [T, {self.NKV}, {self.D}]")
+        vs = _heads(v, "v", dev, shape)
+        at = self._places(block_table, start, cu_seqlens, shape[0])
+        with _Launch(dev, stream, (self.pages, k, v, block_table, start, cu_seqlens)) as st:
+            _check(lib().moe_cache4_write(ctypes.byref(self._c), k.data_ptr(), ks, v.data_ptr(), vs,
+                                          *at, st), "moe_cache4_write")
+
+    def read(self, block_table, start, cu_seqlens, T, k=None, v=None, stream=None):
+        """(k, v) bfloat16 [T, NKV, D]: the values that the cache holds of
+        packed sequences, token i of sequence b from position start[b] + i;
+        places that ``write`` would skip read as zeros.  Rows behind the last
+        sequence are left as they were in a given k and v, and zero in new
+        ones."""
+        dev = self.pages.device
+        shape = (T, self.NKV, self.D)
+        at = self._places(block_table, start, cu_seqlens, T)
+        if (k is None) != (v is None):
+            raise ValueError("give both k and v or neither")
+        fresh = k is None
+        with _Launch(dev, stream, (self.pages, block_table, start, cu_seqlens, k, v)) as st:
+            if fresh:
+                k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+                v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            ks, vs = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
+            _check(lib().moe_cache4_read(ctypes.byref(self._c), k.data_ptr(), ks, v.data_ptr(), vs,
+                                         *at, int(fresh), st), "moe_cache4_read")
+        return k, v
+
+    def attend(self, q, block_table, lens, scale=None, out=None, return_lse=False, stream=None):
+        """out [B, NHq, D] bfloat16 of one query token per sequence, q
+        [B, NHq, D], over the first lens[b] tokens (int32 [B]) of each: query
+        head h reads head h // (NHq / NKV) of the cache, scores are scaled by
+        ``scale`` (default 1 / sqrt(D)).  With ``return_lse`` (out, lse), lse
+        [B, NHq] float32 the logarithm of the sum of the exponentials.  A
+        sequence without tokens gives zeros and -inf."""
+        dev = self.pages.device
+        qs = _heads(q, "q", dev)
+        B, NHq, D = q.shape
+        if D != self.D:
+            raise ValueError(f"q must be [B, heads, {self.D}]")
+        lp = _vector(lens, torch.int32, B, "lens", dev)
+        tp, ts, n = self._table(block_table, B)
+        L = lib()
+        with _Launch(dev, stream, (self.pages, q, block_table, lens, out)) as st:
+            if out is None:
+                out = torch.empty(B, NHq, D, dtype=torch.bfloat16, device=dev)
+                os_ = NHq * D
+            else:
+                os_ = _heads(out, "out", dev, (B, NHq, D))
+                _no_overlap(out, (q, self.pages), "out")
+            lse = torch.empty(B, NHq, dtype=torch.float32, device=dev) if return_lse else None
+            nbytes = int(L.moe_cache4_attend_workspace_bytes(ctypes.byref(self._c), B, NHq, n))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+            _check(L.moe_cache4_attend(
+                ctypes.byref(self._c), q.data_ptr(), qs, tp, ts, n, lp, B, NHq,
+                D ** -0.5 if scale is None else scale, out.data_ptr(), os_, _ptr(lse), _ptr(ws),
+                nbytes, st), "moe_cache4_attend")
+        return (out, lse) if return_lse else out
+
+
+def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=None, out=None,
+                     return_lse=False, stream=None):
+    """out [Tq, NHq, D] bfloat16: attention of packed prompts with query heads
+    q [Tq, NHq, D] over key and value heads k, v [Tk, NKV, D] (token rows may
+    be strided).  Sequence b has the queries cu_seqlens[b] .. cu_seqlens[b + 1]
+    (int32 [B + 1]) and the keys of cu_seqlens_k likewise (default: the same);
+    causal: its last query sees its last key.  Scores are scaled by ``scale``
+    (default 1 / sqrt(D)).  With ``return_lse`` (out, lse), lse [Tq, NHq]
+    float32.  A query that sees nothing gives zeros and -inf.  Rows behind the
+    last sequence are left as they were in a given ``out``, zero in a new one
+    and -inf in lse."""
+    qs = _heads(q, "q")
+    dev = q.device
+    Tq, NHq, D = q.shape
+    ks = _heads(k, "k", dev)
+    Tk, NKV, Dk = k.shape
+    if Dk != D:
+        raise ValueError(f"k must be [Tk, heads, {D}]")
+    vs = _heads(v, "v", dev, (Tk, NKV, D))
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    B = cu_seqlens.shape[0] - 1
+    cq = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
+    if cu_seqlens_k is None:
+        if Tk != Tq:
+            raise ValueError("k has other rows than q: cu_seqlens_k is needed")
+        cu_seqlens_k = cu_seqlens
+    ck = _vector(cu_seqlens_k, torch.int32, B + 1, "cu_seqlens_k", dev)
+    fresh = out is None
+    with _Launch(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out)) as st:
+        if fresh:
+            out = torch.empty(Tq, NHq, D, dtype=torch.bfloat16, device=dev)
+            os_ = NHq * D
+        else:
+            os_ = _heads(out, "out", dev, (Tq, NHq, D))
+            _no_overlap(out, (q, k, v), "out")
+        lse = torch.empty(Tq, NHq, dtype=torch.float32, device=dev) if return_lse else None
+        _check(lib().moe_prompt_attention(
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, B, Tq, Tk, NHq, NKV, D,
+            int(bool(causal)), D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+            _ptr(lse), 3 if fresh else 2, st), "moe_prompt_attention")
+    return (out, lse) if return_lse else out
 
 
 # ------------------------------------------------------------------ a0..a6

@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libmoemi.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "router.hip", "align.hip", "front.hip", "quant.hip", "gemm_decode.hip", "gemm_tile.hip",
-           "down_small.hip", "combine.hip", "rope.hip"]
+           "down_small.hip", "combine.hip", "rope.hip", "qk_norm_rope.hip", "cache4.hip",
+           "cache4_attend.hip", "prompt_attention.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

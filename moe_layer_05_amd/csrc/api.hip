@@ -61,6 +61,10 @@ hipError_t prepare_all() {
   if (e == hipSuccess) e = prepare_down_small_kernels();
   if (e == hipSuccess) e = prepare_combine_kernels();
   if (e == hipSuccess) e = prepare_rope_kernels();
+  if (e == hipSuccess) e = prepare_qk_norm_rope_kernels();
+  if (e == hipSuccess) e = prepare_cache4_kernels();
+  if (e == hipSuccess) e = prepare_cache4_attend_kernels();
+  if (e == hipSuccess) e = prepare_prompt_kernels();
   if (e == hipSuccess) e = hipGetSymbolAddress(&st.scratch, HIP_SYMBOL(scratch));
   if (e == hipSuccess && st.scratch == nullptr) e = hipErrorInvalidSymbol;
   if (e == hipSuccess) st.prepared = true;
@@ -93,6 +97,67 @@ int num_cus() {
 }
 
 moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// Runs a launch on the prepared current device; nothing thrown on the host
+// leaves a C entry.
+template <typename F>
+moe_status guarded(F&& launch) {
+  try {
+    if (prepare_all() != hipSuccess) return MOE_ERR_HIP;
+    return hip_status(launch());
+  } catch (...) {
+    return MOE_ERR_HIP;
+  }
+}
+
+// Token stride of [T][heads][D] bfloat16 rows that are read 16 bytes at a time.
+bool stride_ok(int64_t stride, int64_t heads, int64_t D) {
+  return stride >= heads * D && stride % 8 == 0;
+}
+bool head_size_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
+// Scores are compared before they are scaled, so the scale is positive.
+bool scale_ok(float s) { return s > 0.0f && s <= 3.0e38f; }
+
+bool cache4_shape_ok(int page_size, int NKV, int D) {
+  return page_size > 0 && page_size % 16 == 0 && page_size <= 4096 && NKV > 0 && NKV <= 65535 &&
+         head_size_ok(D);
+}
+moe_status check_cache4(const moe_cache4* c) {
+  if (!c) return MOE_ERR_NULL;
+  if (c->num_pages <= 0 || c->page_size <= 0 || c->NKV <= 0 || c->D <= 0) return MOE_ERR_SHAPE;
+  if (!cache4_shape_ok(c->page_size, c->NKV, c->D) || c->num_pages >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+Cache4 cache4_of(const moe_cache4& c) {
+  return Cache4{static_cast<uint8_t*>(c.pages), c.num_pages, c.page_size / 16, c.NKV, c.D};
+}
+moe_status check_cache_places(const moe_cache4* c, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* table, int64_t table_stride,
+                              int32_t max_pages, const int32_t* start, const int32_t* cu, int32_t B,
+                              int64_t T) {
+  const moe_status st = check_cache4(c);
+  if (st != MOE_OK) return st;
+  if (B < 0 || T < 0 || max_pages < 0 || table_stride < max_pages) return MOE_ERR_SHAPE;
+  if (!cu && T != B) return MOE_ERR_SHAPE;
+  if (T >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(k_stride, c->NKV, c->D) || !stride_ok(v_stride, c->NKV, c->D))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!c->pages || !k || !v || (B > 0 && !start) || (B > 0 && max_pages > 0 && !table))
+    return MOE_ERR_NULL;
+  if (!aligned16(c->pages) || !aligned16(k) || !aligned16(v)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+moe_status check_attend_shape(const moe_cache4* c, int32_t B, int32_t NHq, int32_t max_pages) {
+  const moe_status st = check_cache4(c);
+  if (st != MOE_OK) return st;
+  if (B < 0 || NHq <= 0 || max_pages < 0 || NHq % c->NKV != 0) return MOE_ERR_SHAPE;
+  if (B > 65535 || (int64_t)NHq / 16 + c->NKV > 65535) return MOE_ERR_UNSUPPORTED;
+  // the page of a tile is found by a multiplication that is exact up to here
+  if ((int64_t)max_pages * c->page_size > ((int64_t)1 << 28)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
 
 bool block_m_ok(int bm) { return bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256; }
 
@@ -595,6 +660,143 @@ moe_status moe_inv_rope_fp8_quant_per_head(const void* x, int64_t x_token_stride
   return hip_status(launch_inv_rope_quant(fmt_of(fmt), interleaved != 0, x, x_token_stride,
                                           positions, cos_sin, max_pos, T, NH, D, R, codes,
                                           scales, num_cus(), stream));
+}
+
+moe_status moe_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const int64_t* positions, const float* cos_sin, int64_t max_pos,
+                            int64_t T, int32_t NHq, int32_t NHk, int32_t D, int32_t R,
+                            int32_t interleaved, const void* q_weight, const void* k_weight,
+                            int32_t weights_f32, float eps, void* q_out, int64_t q_out_stride,
+                            void* k_out, int64_t k_out_stride, hipStream_t stream) {
+  if (T < 0 || NHq <= 0 || NHk < 0 || D <= 0 || R <= 0 || max_pos <= 0) return MOE_ERR_SHAPE;
+  if (R > D || (R & 1)) return MOE_ERR_SHAPE;
+  if (D % 8 != 0 || D > 512) return MOE_ERR_UNSUPPORTED;
+  if (interleaved ? (R % 8 != 0) : (R % 16 != 0)) return MOE_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f && eps <= 3.0e38f)) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(q_stride, NHq, D) || !stride_ok(q_out_stride, NHq, D)) return MOE_ERR_UNSUPPORTED;
+  if (NHk && (!stride_ok(k_stride, NHk, D) || !stride_ok(k_out_stride, NHk, D)))
+    return MOE_ERR_UNSUPPORTED;
+  if (T >= ((int64_t)1 << 32) / (NHq + (int64_t)NHk)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!q || !positions || !cos_sin || !q_out || (NHk && (!k || !k_out))) return MOE_ERR_NULL;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(q_weight) ||
+      (NHk && (!aligned16(k) || !aligned16(k_out) || !aligned16(k_weight))))
+    return MOE_ERR_UNSUPPORTED;
+  return guarded([&] {
+    const HeadRows qr{q, q_stride, q_out, q_out_stride, q_weight, NHq};
+    const HeadRows kr{k, k_stride, k_out, k_out_stride, NHk ? k_weight : nullptr, NHk};
+    return launch_qk_norm_rope(qr, kr, positions, cos_sin, max_pos, T, D, R, interleaved != 0,
+                               weights_f32 != 0, eps, num_cus(), stream);
+  });
+}
+
+size_t moe_cache4_page_bytes(int32_t page_size, int32_t NKV, int32_t D) {
+  if (!cache4_shape_ok(page_size, NKV, D)) return 0;
+  return (size_t)NKV * (page_size / 16) * 17 * D;
+}
+
+moe_status moe_cache4_write(const moe_cache4* cache, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const int32_t* block_table,
+                            int64_t table_stride, int32_t max_pages, const int32_t* start,
+                            const int32_t* cu_seqlens, int32_t B, int64_t T, hipStream_t stream) {
+  const moe_status st = check_cache_places(cache, k, k_stride, v, v_stride, block_table,
+                                           table_stride, max_pages, start, cu_seqlens, B, T);
+  if (st != MOE_OK || T == 0) return st;
+  return guarded([&] {
+    return launch_cache4_write(cache4_of(*cache),
+                               CachePlaces{block_table, table_stride, max_pages, start, cu_seqlens, B, T},
+                               k, k_stride, v, v_stride, stream);
+  });
+}
+
+moe_status moe_cache4_read(const moe_cache4* cache, void* k, int64_t k_stride, void* v,
+                           int64_t v_stride, const int32_t* block_table, int64_t table_stride,
+                           int32_t max_pages, const int32_t* start, const int32_t* cu_seqlens,
+                           int32_t B, int64_t T, int32_t zero_tail, hipStream_t stream) {
+  const moe_status st = check_cache_places(cache, k, k_stride, v, v_stride, block_table,
+                                           table_stride, max_pages, start, cu_seqlens, B, T);
+  if (st != MOE_OK || T == 0) return st;
+  return guarded([&] {
+    return launch_cache4_read(cache4_of(*cache),
+                              CachePlaces{block_table, table_stride, max_pages, start, cu_seqlens, B, T},
+                              k, k_stride, v, v_stride, zero_tail != 0, stream);
+  });
+}
+
+size_t moe_cache4_attend_workspace_bytes(const moe_cache4* cache, int32_t B, int32_t NHq,
+                                         int32_t max_pages) {
+  if (check_attend_shape(cache, B, NHq, max_pages) != MOE_OK || B == 0) return 0;
+  const int splits = cache4_attend_splits(B, NHq, cache->NKV, (int64_t)max_pages * cache->page_size);
+  return cache4_attend_workspace(B, NHq, cache->D, splits);
+}
+
+moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_stride,
+                             const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                             const int32_t* lens, int32_t B, int32_t NHq, float scale, void* out,
+                             int64_t out_stride, float* lse, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  const moe_status st = check_attend_shape(cache, B, NHq, max_pages);
+  if (st != MOE_OK) return st;
+  if (table_stride < max_pages) return MOE_ERR_SHAPE;
+  if (!scale_ok(scale)) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(q_stride, NHq, cache->D) || !stride_ok(out_stride, NHq, cache->D))
+    return MOE_ERR_UNSUPPORTED;
+  if (B == 0) return MOE_OK;
+  if (!cache->pages || !q || !lens || !out || (max_pages > 0 && !block_table)) return MOE_ERR_NULL;
+  if (!aligned16(cache->pages) || !aligned16(q) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+  const int splits = cache4_attend_splits(B, NHq, cache->NKV, (int64_t)max_pages * cache->page_size);
+  const size_t need = cache4_attend_workspace(B, NHq, cache->D, splits);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return MOE_ERR_UNSUPPORTED;
+  return guarded([&] {
+    return launch_cache4_attend(cache4_of(*cache), q, q_stride, block_table, table_stride, max_pages,
+                                lens, B, NHq, scale, out, out_stride, lse, splits, workspace, stream);
+  });
+}
+
+moe_status moe_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int32_t* cu_q,
+                                const int32_t* cu_k, int32_t B, int64_t Tq, int64_t Tk,
+                                int32_t NHq, int32_t NKV, int32_t D, int32_t causal, float scale,
+                                void* out, int64_t out_stride, float* lse, int32_t zero_tail,
+                                hipStream_t stream) {
+  if (B < 0 || Tq < 0 || Tk < 0 || NHq <= 0 || NKV <= 0 || D <= 0) return MOE_ERR_SHAPE;
+  if (NHq % NKV != 0) return MOE_ERR_SHAPE;
+  if (!head_size_ok(D) || !scale_ok(scale) || (zero_tail & ~3)) return MOE_ERR_UNSUPPORTED;
+  const int64_t most = ((int64_t)1 << 31) - (1 << 16);
+  if (Tq >= most || Tk >= most) return MOE_ERR_UNSUPPORTED;
+  if ((Tq / 32 + B + 8) * NHq >= most) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(q_stride, NHq, D) || !stride_ok(out_stride, NHq, D) ||
+      !stride_ok(k_stride, NKV, D) || !stride_ok(v_stride, NKV, D))
+    return MOE_ERR_UNSUPPORTED;
+  if (Tq == 0) return MOE_OK;
+  if (B == 0 && !zero_tail) return MOE_OK;
+  if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v))) return MOE_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+  return guarded([&] {
+    PromptArgs p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.out_stride = out_stride;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.B = B;
+    p.NHq = NHq;
+    p.NKV = NKV;
+    p.D = D;
+    p.causal = causal != 0;
+    p.zero_tail = zero_tail;
+    p.scale = scale;
+    return launch_prompt_attention(p, stream);
+  });
 }
 
 moe_status moe_fused_forward_noalloc(const moe_fused_args* a, hipStream_t stream) {

@@ -37,6 +37,15 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float f) {
   return u >> 16;
 }
 
+// Two float32 as bfloat16 in one word, the first low, nearest even; a NaN
+// stays a NaN (one conversion instruction).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2f f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, v2bf));
+}
+
 // Four consecutive partial outputs at element `idx` of a partial-row buffer:
 // float32, or bfloat16 (nearest even) when `bf16`.
 __device__ __forceinline__ void store_part4(void* buf, bool bf16, int64_t idx, float a, float b,

@@ -129,6 +129,10 @@ hipError_t prepare_front_kernels();
 hipError_t prepare_quant_kernels();
 hipError_t prepare_combine_kernels();
 hipError_t prepare_rope_kernels();
+hipError_t prepare_qk_norm_rope_kernels();
+hipError_t prepare_cache4_kernels();
+hipError_t prepare_cache4_attend_kernels();
+hipError_t prepare_prompt_kernels();
 
 // Inverse rotary embedding of [T][NH][D] bfloat16 heads (token stride x_stride
 // elements) with the cos/sin table [max_pos][R], then one FP8 scale per
@@ -137,6 +141,70 @@ hipError_t launch_inv_rope_quant(int fmt, bool interleaved, const void* x, int64
                                  const int64_t* positions, const float* table, int64_t max_pos,
                                  int64_t T, int NH, int D, int R, uint8_t* codes, float* scales,
                                  int num_cus, hipStream_t stream);
+
+// Heads of every token, bfloat16 [T][heads][D] with a token stride in
+// elements, read from x and written to y; weight: the norm's [D], or null.
+struct HeadRows {
+  const void* x;
+  int64_t x_stride;
+  void* y;
+  int64_t y_stride;
+  const void* weight;
+  int heads;
+};
+// RMS norm (where a weight is given) and rotary embedding of the query and
+// key heads; weights bfloat16, or float32 with weights_f32.
+hipError_t launch_qk_norm_rope(const HeadRows& q, const HeadRows& k, const int64_t* positions,
+                               const float* table, int64_t max_pos, int64_t T, int D, int R,
+                               bool interleaved, bool weights_f32, float eps, int num_cus,
+                               hipStream_t stream);
+
+// The paged 4-bit cache (cache4_device.hpp has its layout) and the places of
+// packed tokens in it: token cu[b] + i of sequence b is at its position
+// start[b] + i; cu null: token b is sequence b's only one.
+struct Cache4 {
+  uint8_t* pages;
+  int64_t num_pages;
+  int page_tiles;              // 16-token tiles of a page
+  int NKV, D;
+};
+struct CachePlaces {
+  const int32_t* table;        // [B][max_pages] page ids, row stride table_stride
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* start;        // [B]
+  const int32_t* cu;           // [B + 1] or null
+  int B;
+  int64_t T;
+};
+hipError_t launch_cache4_write(const Cache4& c, const CachePlaces& at, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride,
+                               hipStream_t stream);
+hipError_t launch_cache4_read(const Cache4& c, const CachePlaces& at, void* k, int64_t k_stride,
+                              void* v, int64_t v_stride, bool zero_tail, hipStream_t stream);
+
+// One query token per sequence over the cache.  splits > 1 needs
+// cache4_attend_workspace(...) bytes of scratch.
+int cache4_attend_splits(int64_t B, int NHq, int NKV, int64_t capacity);
+size_t cache4_attend_workspace(int64_t B, int NHq, int D, int splits);
+hipError_t launch_cache4_attend(const Cache4& c, const void* q, int64_t q_stride,
+                                const int32_t* table, int64_t table_stride, int max_pages,
+                                const int32_t* lens, int B, int NHq, float scale, void* out,
+                                int64_t out_stride, float* lse, int splits, void* workspace,
+                                hipStream_t stream);
+
+struct PromptArgs {
+  const uint16_t *q, *k, *v;   // [Tq][NHq][D], [Tk][NKV][D] bfloat16
+  int64_t q_stride, k_stride, v_stride, out_stride;   // token strides, elements
+  const int32_t *cu_q, *cu_k;  // [B + 1]
+  uint16_t* out;               // [Tq][NHq][D]
+  float* lse;                  // [Tq][NHq] or null
+  int64_t Tq, Tk;
+  int B, NHq, NKV, D;
+  int causal, zero_tail;
+  float scale;
+};
+hipError_t launch_prompt_attention(const PromptArgs& p, hipStream_t stream);
 
 // The shape is chosen for num_cus compute units (the current device's);
 // nblk_cap is the layout's block capacity, est_blocks the blocks a call

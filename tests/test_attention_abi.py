@@ -1,0 +1,153 @@
+"""Refusals of the attention side's entry points: every check runs on the host
+before any HIP call, so wrong calls are shown here without a GPU."""
+
+import ctypes
+
+import pytest
+import torch
+
+import moe_layer_05_amd as mm
+from moe_layer_05_amd import binding
+
+OK, NULL, SHAPE, UNSUP, WS = 0, 1, 2, 3, 4
+P = 4096                       # a stand-in for an aligned device pointer; never read
+
+
+@pytest.fixture(scope="module")
+def L():
+    return binding.lib()
+
+
+def norm_rope(L, **kw):
+    a = dict(q=P, qs=256, k=P, ks=128, pos=P, cs=P, max_pos=10, T=3, NHq=2, NHk=1, D=128, R=128,
+             inter=0, qw=P, kw=P, f32=0, eps=1e-6, qo=P, qos=256, ko=P, kos=128)
+    a.update(kw)
+    return L.moe_qk_norm_rope(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), SHAPE), (dict(NHq=0), SHAPE), (dict(NHk=-1), SHAPE), (dict(R=0), SHAPE),
+    (dict(R=144), SHAPE), (dict(R=33), SHAPE), (dict(max_pos=0), SHAPE), (dict(D=0), SHAPE),
+    (dict(D=132), UNSUP), (dict(D=520, R=64, qs=2080, ks=2080, qos=2080, kos=2080), UNSUP),
+    (dict(R=24), UNSUP), (dict(R=12, inter=1), UNSUP), (dict(eps=-1.0), UNSUP),
+    (dict(eps=float("nan")), UNSUP), (dict(eps=float("inf")), UNSUP), (dict(qs=248), UNSUP),
+    (dict(qs=260), UNSUP), (dict(ks=120), UNSUP), (dict(qos=255), UNSUP), (dict(kos=64), UNSUP),
+    (dict(T=1 << 31), UNSUP), (dict(q=0), NULL), (dict(k=0), NULL), (dict(pos=0), NULL),
+    (dict(cs=0), NULL), (dict(qo=0), NULL), (dict(ko=0), NULL), (dict(q=P + 8), UNSUP),
+    (dict(qw=P + 2), UNSUP), (dict(ko=P + 4), UNSUP), (dict(T=0), OK),
+    (dict(T=0, NHk=0, k=0, ko=0, kw=0, ks=0, kos=0), OK),
+])
+def test_norm_rope(L, kw, want):
+    assert norm_rope(L, **kw) == want
+
+
+def cache(pages=P, n=4, size=16, heads=2, D=128):
+    return ctypes.byref(binding.Cache4(pages, n, size, heads, D))
+
+
+CACHES = [(dict(n=0), SHAPE), (dict(size=0), SHAPE), (dict(heads=0), SHAPE), (dict(D=-64), SHAPE),
+          (dict(size=24), UNSUP), (dict(size=8192), UNSUP), (dict(D=96), UNSUP), (dict(D=512), UNSUP),
+          (dict(n=1 << 31), UNSUP), (dict(heads=70000), UNSUP)]
+
+
+def places(fn, c, more=(), **kw):
+    a = dict(k=P, ks=256, v=P, vs=256, table=P, ts=5, pages=5, start=P, cu=P, B=2, T=9)
+    a.update(kw)
+    return fn(c, *a.values(), *more, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(pages=-1), SHAPE), (dict(ts=4), SHAPE),
+    (dict(cu=None), SHAPE), (dict(T=1 << 31), UNSUP), (dict(ks=128), UNSUP), (dict(vs=260), UNSUP),
+    (dict(k=None), NULL), (dict(v=None), NULL), (dict(table=None), NULL), (dict(start=None), NULL),
+    (dict(k=P + 2), UNSUP), (dict(v=P + 8), UNSUP), (dict(T=0), OK), (dict(T=0, B=0, cu=None), OK),
+])
+def test_cache_write_and_read(L, kw, want):
+    assert places(L.moe_cache4_write, cache(), **kw) == want
+    assert places(L.moe_cache4_read, cache(), more=(0,), **kw) == want
+
+
+@pytest.mark.parametrize("c,want", CACHES + [(dict(pages=None), NULL), (dict(pages=P + 8), UNSUP)])
+def test_cache_shapes(L, c, want):
+    assert places(L.moe_cache4_write, cache(**c)) == want
+    assert places(L.moe_cache4_read, cache(**c), more=(0,)) == want
+    if "D" not in c and "heads" not in c:
+        assert attend(L, cache(**c)) == want
+
+
+def test_cache_null(L):
+    assert places(L.moe_cache4_write, None) == NULL
+    assert attend(L, None) == NULL
+    assert L.moe_cache4_attend_workspace_bytes(None, 1, 2, 1) == 0
+
+
+def attend(L, c, **kw):
+    a = dict(q=P, qs=512, table=P, ts=5, pages=5, lens=P, B=2, NHq=4, scale=0.1, out=P, os=512,
+             lse=None, ws=P, wsb=1 << 40)
+    a.update(kw)
+    return L.moe_cache4_attend(c, *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), SHAPE), (dict(NHq=0), SHAPE), (dict(NHq=3), SHAPE), (dict(pages=-1), SHAPE),
+    (dict(ts=4), SHAPE), (dict(B=70000), UNSUP), (dict(pages=(1 << 24) + 1, ts=1 << 30), UNSUP),
+    (dict(scale=0.0), UNSUP), (dict(scale=-1.0), UNSUP), (dict(scale=float("nan")), UNSUP),
+    (dict(scale=float("inf")), UNSUP), (dict(qs=384), UNSUP), (dict(os=516), UNSUP),
+    (dict(q=None), NULL), (dict(lens=None), NULL), (dict(out=None), NULL), (dict(table=None), NULL),
+    (dict(q=P + 4), UNSUP), (dict(out=P + 8), UNSUP), (dict(B=0), OK),
+    (dict(pages=1000, ts=1000, ws=None), WS), (dict(pages=1000, ts=1000, wsb=16), WS),
+    (dict(pages=1000, ts=1000, ws=P + 8), UNSUP),
+])
+def test_attend(L, kw, want):
+    assert attend(L, cache(), **kw) == want
+
+
+def test_attend_workspace(L):
+    need = L.moe_cache4_attend_workspace_bytes
+    assert need(cache(), 0, 4, 1000) == 0 and need(cache(), 2, 3, 1000) == 0
+    assert need(cache(), 2, 4, 1) == 0                     # one split: nothing to join
+    assert need(cache(), 1, 4, 1000) > 0
+    a, b = need(cache(), 1, 4, 1000), need(cache(), 1, 8, 1000)
+    assert b == 2 * a
+
+
+def prompt(L, **kw):
+    a = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cq=P, ck=P, B=2, Tq=9, Tk=9, NHq=4, NKV=2, D=128,
+             causal=1, scale=0.1, out=P, os=512, lse=None, tail=0)
+    a.update(kw)
+    return L.moe_prompt_attention(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), SHAPE), (dict(Tq=-1), SHAPE), (dict(Tk=-1), SHAPE), (dict(NHq=3), SHAPE),
+    (dict(NKV=0), SHAPE), (dict(D=0), SHAPE), (dict(D=80), UNSUP), (dict(scale=0.0), UNSUP),
+    (dict(scale=float("nan")), UNSUP), (dict(Tq=(1 << 31) - 1), UNSUP), (dict(Tk=1 << 31), UNSUP),
+    (dict(Tq=1 << 30, NHq=128, qs=16384, os=16384), UNSUP), (dict(qs=384), UNSUP),
+    (dict(ks=250), UNSUP), (dict(vs=128), UNSUP), (dict(os=513), UNSUP), (dict(tail=4), UNSUP),
+    (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(cq=None), NULL),
+    (dict(ck=None), NULL), (dict(out=None), NULL), (dict(q=P + 8), UNSUP), (dict(v=P + 2), UNSUP),
+    (dict(Tq=0), OK), (dict(B=0), OK),
+])
+def test_prompt(L, kw, want):
+    assert prompt(L, **kw) == want
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    i32 = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        mm.qk_norm_rope(x, x, torch.zeros(3, dtype=torch.int64), torch.zeros(4, 64), 64)
+    with pytest.raises(TypeError):
+        mm.prompt_attention(x, x, x, i32)
+    with pytest.raises(TypeError):
+        mm.KVCache4.of(torch.zeros(2, 2, 1, 17 * 64, dtype=torch.uint8))
+    with pytest.raises(mm.MoEError):
+        mm.KVCache4(4, 24, 2, 128)
+    with pytest.raises(mm.MoEError):
+        mm.KVCache4(0, 16, 2, 128)
+
+
+def test_struct_layout():
+    F = binding.Cache4
+    assert [getattr(F, n).offset for n, _ in F._fields_] == [0, 8, 16, 20, 24]
+    assert ctypes.sizeof(F) == 32
