@@ -512,7 +512,7 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_t
  *   zero_tail     bit 0: rows of out behind the last sequence become 0, bit 1:
  *                 rows of lse behind it become -inf
  * Supported: D 64, 128, 192 or 256; NHq a multiple of NKV; scale positive and
- * finite; Tq, Tk < 2^31 - 2^16; (Tq / 32 + B) * NHq < 2^31.
+ * finite; k and v token strides <= 2^24; Tq, Tk < 2^31 - 2^16; (Tq / 32 + B) * NHq < 2^31.
  */
 moe_status moe_prompt_attention(const void* q, int64_t q_token_stride, const void* k,
                                 int64_t k_token_stride, const void* v, int64_t v_token_stride,

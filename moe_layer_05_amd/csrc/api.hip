@@ -769,6 +769,8 @@ moe_status moe_prompt_attention(const void* q, int64_t q_stride, const void* k, 
   if (!stride_ok(q_stride, NHq, D) || !stride_ok(out_stride, NHq, D) ||
       !stride_ok(k_stride, NKV, D) || !stride_ok(v_stride, NKV, D))
     return MOE_ERR_UNSUPPORTED;
+  // 32-bit byte offsets inside a tile of keys
+  if (k_stride > (1 << 24) || v_stride > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   if (Tq == 0) return MOE_OK;
   if (B == 0 && !zero_tail) return MOE_OK;
   if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v))) return MOE_ERR_NULL;

@@ -25,28 +25,37 @@
 // maximum moves only when a score passes it by more than 8 (in powers of
 // two), so most tiles skip the rescaling of O^T.
 //
-// Work split: a workgroup of four waves takes 128 query rows of one head, 32
-// rows a wave; K and V tiles are shared through LDS, two deep: the next tile's
-// loads are in flight in registers while the current one is worked on.  LDS
-// rows keep their 16-byte pieces XOR-ed with the row so that both the row
-// reads of K and the transposing reads of V are free of bank conflicts.
-// Each XCD takes a contiguous range of (head, tile) so that a kv head's keys
-// stay in one L2; inside a sequence the tiles with the most keys go first.
+// Work split: a workgroup of eight waves takes 256 query rows of one head, 32
+// rows a wave.  K and V tiles of 64 keys (32 for D = 192, 256) come to LDS by
+// direct loads into a ring of four, two tiles ahead; rows behind the last key
+// repeat it.  The two waves of a SIMD work in opposite phases (below): a
+// tile's two products are 32 matrix instructions (D = 128), its softmax about
+// 110 vector instructions of which 32 are exponentials, so neither may wait
+// for the other.  Each XCD takes a contiguous range of (head, tile) so that a
+// kv head's keys stay in one L2; inside a sequence the tiles with the most
+// keys go first.
+//
+// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 545 us = 1.01
+// PFLOP/s (D = 64, 192, 256: 0.72, 1.05, 1.12; not causal, D = 128: 1.11); a
+// library product of 8192^3 reaches 1.38 on the same card, the matrix
+// instructions of this kernel alone (no LDS reads, no softmax) 1.68.  Without
+// the softmax it takes 0.88 of its time, without the loads to LDS 0.94: what
+// bounds it is the phase of the products with its LDS reads (32 rows a wave:
+// one 16-byte read per matrix instruction).
 //
 // A key or value that a row does not see never reaches it: scores of masked
-// pairs are replaced, and as 0 * NaN is NaN, a workgroup that ends with a
-// value that is not finite starts over with the masked tiles' values taken
-// apart (kCareful below); finite inputs never do.
+// pairs are replaced, and a wave that ends with a value that is not finite
+// looks for values among its masked pairs that 0 * NaN carried over
+// (mend_rows).
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "internal.hpp"
 
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * kWave;
 constexpr int kRows = 32;                       // query rows of a wave
-constexpr int kBlockRows = kWaves * kRows;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
@@ -54,51 +63,140 @@ constexpr float kNegInf = -__builtin_inff();
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) v4s lds_v4s;
+#define MOE_LDS __attribute__((address_space(3)))
 
-// Keys of a tile: 64, or 32 where two tiles of 64 would not leave room for a
-// second workgroup on the compute unit (D = 192, 256).
-template <int D>
-constexpr int tile_keys() { return D <= 128 ? 64 : 32; }
-template <int D>
-constexpr int lds_bytes() { return 2 * 2 * tile_keys<D>() * D * 2; }
+// Shape of a kernel: head size, waves of a workgroup, buffers of the ring.
+template <int D_, int WAVES_, int BUFS_>
+struct Shape {
+  static constexpr int D = D_, kWaves = WAVES_, kBufs = BUFS_;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int kBlockRows = kWaves * kRows;
+  // keys of a tile
+  static constexpr int KB = D <= 128 ? 64 : 32;
+  static constexpr int kRowBytes = 2 * D;
+  static constexpr int kHalf = KB * kRowBytes;            // K (or V) of a tile
+  static constexpr int kLoads = 2 * kHalf / 1024 / kWaves;  // 1 KB loads of a wave per tile
+  static constexpr int kAhead = kBufs - 2;                // tiles in flight
+  static constexpr int kLds = kBufs * 2 * kHalf;
+  static_assert(2 * kHalf % (1024 * kWaves) == 0, "whole loads per wave");
+  // operands read ahead, and whether the two products take turns: as far as
+  // the registers go (D = 256 would spill)
+  static constexpr int kReadAhead = D <= 192 ? 4 : 2;
+  static constexpr bool kTurns = D <= 192;
+  // The 16-byte pieces of a row are XOR-ed with a function of the row inside
+  // groups of kGroup.  The 64 banks hold 256 bytes: rows of 256 or 512 bytes
+  // all start at the same bank; 16 rows that read the same piece need 16
+  // different positions, and 4 rows that read 4 pieces each (the transposing
+  // read) need them in 4 different quarters.  Rows of 128 or 384 bytes
+  // alternate between the two halves of the banks.
+  static constexpr int kGroup = D % 128 == 0 ? 16 : 8;
+  __device__ __forceinline__ static int mix(int row) {
+    if constexpr (kGroup == 16) return ((row & 3) << 2) | ((row >> 2) & 3);
+    return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  }
+  // byte of piece p of a row
+  __device__ __forceinline__ static int at(int row, int p) {
+    return row * kRowBytes + (p & ~(kGroup - 1)) * 16 + ((p & (kGroup - 1)) ^ mix(row)) * 16;
+  }
+};
 
-// Position of 16-byte piece p of a row.  The 64 banks hold 256 bytes: rows of
-// 256 or 512 bytes all start at the same bank, and 16 rows that read the same
-// piece need 16 different positions, while 4 rows that read 4 pieces each
-// (the transposing read) need them in 4 different quarters.  Rows of 128 or
-// 384 bytes alternate between the two halves of the banks.
-template <int D>
-__device__ __forceinline__ int swizzle(int p, int row) {
-  if constexpr (D % 128 == 0) return p ^ (((row & 3) << 2) | ((row >> 2) & 3));
-  const int x = row >> 1;
-  return p ^ (((x & 1) << 2) | ((x >> 1) & 3));
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const MOE_LDS uint8_t*)p;
 }
 
+// 1 KB from 64 lanes' addresses (uniform base + 32-bit byte offset) to LDS at
+// `lds` (uniform), lane after lane.  Written in assembly because the compiler
+// would otherwise wait for every such load before its next LDS read; the
+// kernel waits for them itself (wait_loads) and no register is an output.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n"
+               "s_nop 0\n"
+               "global_load_lds_dwordx4 %1, %0"
+               :
+               : "s"(base), "v"(offset), "s"(lds)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// Every wave's LDS accesses so far are done, and those after stay after.
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\ns_barrier" : : : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int ROWS>
 __device__ __forceinline__ int seq_tiles(const PromptArgs& p, int b, int* q0, int* q1) {
   int64_t lo = p.cu_q[b], hi = p.cu_q[b + 1];
   lo = lo < 0 ? 0 : (lo > p.Tq ? p.Tq : lo);
   hi = hi < lo ? lo : (hi > p.Tq ? p.Tq : hi);
   *q0 = (int)lo;
   *q1 = (int)hi;
-  return (int)((hi - lo + kBlockRows - 1) / kBlockRows);
+  return (int)((hi - lo + ROWS - 1) / ROWS);
 }
 
-// Zeroes what is not finite in a word of two bfloat16.
-__device__ __forceinline__ uint32_t only_finite(uint32_t w) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
-  return w;
-}
-
+// Mends a wave's rows q_row .. + rows of head h after their last tile, when one
+// of them holds a value that is not finite.  Row i sees the keys j < lim(i) =
+// clamp(first_lim + i * causal, 0, nk), but its products ran over those up to
+// key_end, with probability 0: where a value in between is not finite,
+// 0 * NaN has reached rows that do not see it.  Those rows are computed again,
+// one lane holding D / 64 features, over exactly the keys they see.  Reached
+// by no finite values; kept out of line so that it costs the others no
+// register.
 template <int D>
-__global__ __launch_bounds__(kThreads, D <= 192 ? 2 : 1) void prompt_attention_kernel(
+__attribute__((noinline)) __device__ void mend_rows(PromptArgs a, int64_t q_row, int rows, int h, int64_t k0,
+                                                    int nk, int key_end, int first_lim, int causal) {
+  constexpr int kPer = D / kWave;
+  const int f0 = (threadIdx.x & (kWave - 1)) * kPer;
+  const int kvh = h / (a.NHq / a.NKV);
+  const float scale2 = a.scale * kLog2e;
+  auto limit = [&](int i) {
+    const int l = first_lim + i * causal;
+    return l < 0 ? 0 : (l > nk ? nk : l);
+  };
+  int bad = -1;                                        // the last key whose value is not finite
+  for (int j = limit(0); j < key_end; ++j) {
+    bool odd = false;
+    for (int d = 0; d < kPer; ++d)
+      odd |= (a.v[(k0 + j) * a.v_stride + (int64_t)kvh * D + f0 + d] & 0x7F80u) == 0x7F80u;
+    if (__any(odd)) bad = j;
+  }
+  for (int i = 0; i < rows && limit(i) <= bad; ++i) {
+    const int64_t row = q_row + i;
+    const int lim = limit(i);
+    float q[kPer], o[kPer], m = kNegInf, l = 0.0f;
+    for (int d = 0; d < kPer; ++d) {
+      q[d] = bf16_lo(a.q[row * a.q_stride + (int64_t)h * D + f0 + d]);
+      o[d] = 0.0f;
+    }
+    for (int j = 0; j < lim; ++j) {
+      const uint16_t* k = a.k + (k0 + j) * a.k_stride + (int64_t)kvh * D + f0;
+      const uint16_t* v = a.v + (k0 + j) * a.v_stride + (int64_t)kvh * D + f0;
+      float s = 0.0f;
+      for (int d = 0; d < kPer; ++d) s = fmaf(q[d], bf16_lo(k[d]), s);
+      s = wave_sum(s) * scale2;
+      const float next = fmaxf(m, s);
+      const float f = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+      const float p = __builtin_amdgcn_exp2f(s - (next == kNegInf ? 0.0f : next));
+      m = next;
+      l = l * f + p;
+      for (int d = 0; d < kPer; ++d) o[d] = o[d] * f + p * bf16_lo(v[d]);
+    }
+    const float f = m == kNegInf ? l : 1.0f / l;
+    for (int d = 0; d < kPer; ++d)
+      a.out[row * a.out_stride + (int64_t)h * D + f0 + d] = (uint16_t)pack_bf16(o[d] * f, 0.0f);
+    if (f0 == 0 && a.lse) a.lse[row * a.NHq + h] = (m + __log2f(l)) * kLn2;
+  }
+}
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_kernel(
     PromptArgs a, int slots, int per_xcd) {
-  constexpr int KB = tile_keys<D>();
+  constexpr int D = S::D, KB = S::KB;
   constexpr int kPieces = D / 8;                      // 16-byte pieces of a row
-  constexpr int kLoads = KB * kPieces / kThreads;     // pieces of a thread, per K or V tile
-  constexpr int kTileHalf = KB * D * 2;               // bytes of K (or V) in a buffer
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -114,7 +212,7 @@ __global__ __launch_bounds__(kThreads, D <= 192 ? 2 : 1) void prompt_attention_k
   int seq = -1, tile = 0, q0 = 0, q1 = 0, total = 0;
   for (int b0 = 0; b0 < a.B; b0 += kWave) {
     int lo = 0, hi = 0;
-    const int nt = b0 + lane < a.B ? seq_tiles(a, b0 + lane, &lo, &hi) : 0;
+    const int nt = b0 + lane < a.B ? seq_tiles<S::kBlockRows>(a, b0 + lane, &lo, &hi) : 0;
     const int incl = wave_inclusive_sum_dpp(nt);
     const unsigned long long hit = __ballot(x >= total + incl - nt && x < total + incl);
     if (hit) {
@@ -153,13 +251,12 @@ __global__ __launch_bounds__(kThreads, D <= 192 ? 2 : 1) void prompt_attention_k
     const int64_t l = (int64_t)i + 1 + nk - nq;
     return l < 0 ? 0 : (l > nk ? nk : (int)l);
   };
-  const int block0 = tile * kBlockRows;
+  const int block0 = tile * S::kBlockRows;
   const int row0 = block0 + wave * kRows;
   const int row = row0 + c;                           // in the sequence; may be past its end
   const int lim = limit(row);
-  const int wave_min = limit(row0);
   const int wave_max = row0 < nq ? limit(min(row0 + kRows, nq) - 1) : 0;
-  const int tiles = (limit(min(block0 + kBlockRows, nq) - 1) + KB - 1) / KB;
+  const int tiles = (limit(min(block0 + S::kBlockRows, nq) - 1) + KB - 1) / KB;
 
   v8bf q[D / 16];
   {
@@ -168,158 +265,237 @@ __global__ __launch_bounds__(kThreads, D <= 192 ? 2 : 1) void prompt_attention_k
     for (int s = 0; s < D / 16; ++s)
       q[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 16 * s));
   }
+  // the queries are in registers before the first load to LDS: waiting for them
+  // later would wait for those loads as well
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
   const float scale2 = a.scale * kLog2e;
   const uint16_t* kbase = a.k + k0 * a.k_stride + (int64_t)kvh * D;
   const uint16_t* vbase = a.v + k0 * a.v_stride + (int64_t)kvh * D;
 
-  uint4 kr[kLoads], vr[kLoads];
+  // This wave's loads of a tile: 1 KB pieces wave, wave + kWaves, .. of K's
+  // and then V's LDS image; the lane brings the 16 bytes that belong there.
+  const uint32_t lds0 = lds_addr(smem);
+  int lrow[S::kLoads];                                // row in the tile
+  uint32_t loff[S::kLoads];                           // byte offset of that row's piece
+#pragma unroll
+  for (int i = 0; i < S::kLoads; ++i) {
+    const int part = wave + i * S::kWaves;
+    const bool is_v = part >= S::kHalf / 1024;
+    const int byte = (part * 1024 + lane * 16) - (is_v ? S::kHalf : 0);
+    const int r = byte / S::kRowBytes, p = (byte - r * S::kRowBytes) / 16;
+    lrow[i] = r;
+    const int piece = (p & ~(S::kGroup - 1)) | ((p & (S::kGroup - 1)) ^ S::mix(r));
+    loff[i] = (uint32_t)r * (uint32_t)(2 * (is_v ? a.v_stride : a.k_stride)) + piece * 16;
+  }
   auto fetch = [&](int t) {
+    const uint32_t buf = lds0 + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
+    const int over = t * KB + KB - nk;                // rows behind the end repeat the last one
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int idx = tid + i * kThreads;
-      const int r = idx / kPieces, pc = idx - r * kPieces;
-      const int64_t j = min(t * KB + r, nk - 1);      // rows behind the end repeat the last one
-      kr[i] = *reinterpret_cast<const uint4*>(kbase + j * a.k_stride + pc * 8);
-      vr[i] = *reinterpret_cast<const uint4*>(vbase + j * a.v_stride + pc * 8);
-    }
-  };
-  auto stash = [&](int buf) {
-    uint8_t* dst = smem + buf * 2 * kTileHalf;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int idx = tid + i * kThreads;
-      const int r = idx / kPieces, pc = idx - r * kPieces;
-      const int at = (r * kPieces + swizzle<D>(pc, r)) * 16;
-      *reinterpret_cast<uint4*>(dst + at) = kr[i];
-      *reinterpret_cast<uint4*>(dst + kTileHalf + at) = vr[i];
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int part = wave + i * S::kWaves;
+      const bool is_v = part >= S::kHalf / 1024;
+      const int64_t stride = is_v ? a.v_stride : a.k_stride;
+      uint32_t off = loff[i];
+      if (over > 0) off -= (uint32_t)max(lrow[i] - (KB - 1 - over), 0) * (uint32_t)(2 * stride);
+      load_to_lds((is_v ? vbase : kbase) + (int64_t)t * KB * stride, off, buf + part * 1024);
     }
   };
 
+  // LDS bytes of the operands: K row c (+ 32 i), piece 2 st + g; V row 16 u +
+  // 4 g + (lane & 15) / 4 (+ 8), piece 4 d + x.  The pieces' XOR with the row
+  // leaves constants in st and d, since rows differ by multiples of 32 or 16,
+  // and 8 rows further on the XOR-ed function differs in bit 1.
+  const int vr = 4 * g + ((lane & 15) >> 2);
+  const uint32_t kat = lds0 + S::at(c, g);
+  const uint32_t vat = lds0 + S::kHalf + S::at(vr, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + (lane & 1) * 8;
+
+  // Tiles that every row of the workgroup sees whole, and this wave's tiles.
+  const int whole = limit(block0) / KB;
+  const int mine = (wave_max + KB - 1) / KB;
   float m, l;
-  v16f o[D / 32];
-  // kCareful: values that are not finite are left out of the masked tiles'
-  // product and added afterwards to the rows that see them.
-  auto attend = [&](bool careful) {
-    m = kNegInf;
-    l = 0.0f;
+  v16f o[D / 32], s[KB / 32];
+  v8bf pb[KB / 16];
+
+  // Operands of the matrix instructions.  Scores of tile t: instruction n
+  // takes K rows 32 i .. of step st; values: V^T rows 32 d .. of 16 keys u.
+  // Neighbours add to different accumulators where there are several.
+  constexpr int kOps = (D / 16) * (KB / 32);           // of either product
+  auto key_operand = [&](uint32_t kt, int n) {
+    const int st = n / (KB / 32), i = n % (KB / 32);
+    const uint32_t at = (kt ^ (32 * (st % (S::kGroup / 2)))) + (2 * st / S::kGroup) * (S::kGroup * 16);
+    return *(const MOE_LDS v8bf*)(uintptr_t)(at + i * 32 * S::kRowBytes);
+  };
+  auto value_operand = [&](uint32_t vt, int n) {
+    const int d = n % (D / 32), u = n / (D / 32);
+    const uint32_t far = (4 * d / S::kGroup) * (S::kGroup * 16) + u * 16 * S::kRowBytes;
+    const uint32_t at0 = (vt ^ (64 * (d % (S::kGroup / 4)))) + far;
+    const uint32_t at1 = ((vt + 8 * S::kRowBytes) ^ (64 * (d % (S::kGroup / 4))) ^ 32) + far;
+    const uint2 v0 = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS v4s*)(uintptr_t)at0));
+    const uint2 v1 = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS v4s*)(uintptr_t)at1));
+    return __builtin_bit_cast(v8bf, make_uint4(v0.x, v0.y, v1.x, v1.y));
+  };
+  // S^T of tile t, and O^T += V^T P^T of tile t - 1 with P as the last softmax
+  // left it, each on request; together they take turns (kTurns), so that an
+  // instruction seldom waits for the one before it.  Operands are read
+  // kReadAhead at a time, one such group ahead of its use.  The wave goes
+  // before the other one of its SIMD meanwhile, whose softmax fills the gaps
+  // (8192 tokens, 32 heads of 128: 543 us, without the priority 561 us).
+  auto multiply = [&](int t, auto scores, auto values) {
+    constexpr bool kS = decltype(scores)::value, kV = decltype(values)::value;
+    constexpr int kAll = (kS ? kOps : 0) + (kV ? kOps : 0), kAt = S::kReadAhead;
+    constexpr bool kTurns = kS && kV && S::kTurns;
+    auto is_score = [&](int n) { return kTurns ? n % 2 == 0 : kS && n < kOps; };
+    auto op_of = [&](int n) { return kTurns ? n / 2 : n % kOps; };
+    const uint32_t kt = kat + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
+    const uint32_t vt = vat + (uint32_t)((t + S::kBufs - 1) % S::kBufs) * (2 * S::kHalf);
+    __builtin_amdgcn_s_setprio(1);
+    v8bf f[2][kAt];
+    auto read = [&](int n) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+      for (int i = 0; i < kAt; ++i) {
+        const int op = op_of(n + i);
+        f[(n / kAt) & 1][i] = is_score(n + i) ? key_operand(kt, op) : value_operand(vt, op);
+      }
+      __builtin_amdgcn_sched_barrier(0);               // reads stay ahead of the products before them
+    };
+    if constexpr (kS) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-    if (tiles > 0) {
-      fetch(0);
-      stash(0);
+      for (int i = 0; i < KB / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[i][r] = 0.0f;
     }
-    __syncthreads();
-    for (int t = 0; t < tiles; ++t) {
-      if (t + 1 < tiles) fetch(t + 1);
-      const uint8_t* kt = smem + (t & 1) * 2 * kTileHalf;
-      const uint8_t* vt = kt + kTileHalf;
-      if (t * KB < wave_max) {                         // wave-uniform
-        v16f s[KB / 32];
+    read(0);
 #pragma unroll
-        for (int i = 0; i < KB / 32; ++i)
+    for (int n = 0; n < kAll; n += kAt) {
+      if (n + kAt < kAll) read(n + kAt);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) s[i][r] = 0.0f;
-#pragma unroll
-        for (int st = 0; st < D / 16; ++st) {
-#pragma unroll
-          for (int i = 0; i < KB / 32; ++i) {
-            const int r = i * 32 + c;
-            const uint4 kf = *reinterpret_cast<const uint4*>(
-                kt + (r * kPieces + swizzle<D>(2 * st + g, r)) * 16);
-            s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, kf), q[st], s[i], 0, 0, 0);
-          }
-        }
-        const bool masked = (t + 1) * KB > wave_min;
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < KB / 32; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int key = t * KB + i * 32 + 8 * (r >> 2) + 4 * g + (r & 3);
-              if (key >= lim) s[i][r] = kNegInf;
-            }
-        }
-        float top = s[0][0];
-#pragma unroll
-        for (int i = 0; i < KB / 32; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
-        top *= scale2;
-        if (__any(top > m + kSlack)) {
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float next = fmaxf(m, top);
-          const float f = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - next);
-          m = next;
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[i][r] *= f;
-        }
-        const float base = m == kNegInf ? 0.0f : -m;
-        float sum = 0.0f;
-        v8bf pb[KB / 16];
-#pragma unroll
-        for (int u = 0; u < KB / 16; ++u) {
-          uint32_t pw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = (u & 1) * 8 + 2 * i;
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u >> 1][r], scale2, base));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u >> 1][r + 1], scale2, base));
-            sum += p0 + p1;
-            pw[i] = pack_bf16(p0, p1);
-          }
-          pb[u] = __builtin_bit_cast(v8bf, make_uint4(pw[0], pw[1], pw[2], pw[3]));
-        }
-        l += sum;
-#pragma unroll
-        for (int u = 0; u < KB / 16; ++u) {
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d) {
-            // lane: key row r0 (+ 8), features 8 * (piece) + 4 * (lane & 1) ..
-            const int r0 = 16 * u + 4 * g + ((lane & 15) >> 2);
-            const int pc = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-            const uint8_t* a0 = vt + (r0 * kPieces + swizzle<D>(pc, r0)) * 16 + (lane & 1) * 8;
-            const uint8_t* a1 = vt + ((r0 + 8) * kPieces + swizzle<D>(pc, r0 + 8)) * 16 + (lane & 1) * 8;
-            const uint2 v0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a0));
-            const uint2 v1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)a1));
-            uint4 vf = make_uint4(v0.x, v0.y, v1.x, v1.y);
-            if (careful && masked)
-              vf = make_uint4(only_finite(vf.x), only_finite(vf.y), only_finite(vf.z), only_finite(vf.w));
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, vf), pb[u], o[d], 0, 0, 0);
-          }
-        }
-        if (careful && masked) {
-          for (int key = 0; key < KB && t * KB + key < nk; ++key) {
-            const bool seen = t * KB + key < lim;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const int f = 32 * d + 8 * (r >> 2) + 4 * g + (r & 3);
-                const uint16_t bits = *reinterpret_cast<const uint16_t*>(
-                    vt + (key * kPieces + swizzle<D>(f >> 3, key)) * 16 + (f & 7) * 2);
-                if (seen && (bits & 0x7F80u) == 0x7F80u) o[d][r] += bf16_lo(bits);
-              }
-          }
+      for (int i = 0; i < kAt; ++i) {
+        const int op = op_of(n + i);
+        const v8bf x = f[(n / kAt) & 1][i];
+        if (is_score(n + i)) {
+          const int j = op % (KB / 32);
+          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[op / (KB / 32)], s[j], 0, 0, 0);
+        } else {
+          const int d = op % (D / 32);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, pb[op / (D / 32)], o[d], 0, 0, 0);
         }
       }
-      if (t + 1 < tiles) stash((t + 1) & 1);
-      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
+  };
+  // P of S^T, with the running maximum and sum.
+  auto softmax = [&](int t) {
+    if (t >= whole) {                                  // uniform
+      const int left = lim - t * KB - 4 * g;           // of this lane's keys, from register 0's on
+#pragma unroll
+      for (int i = 0; i < KB / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[i][r] = i * 32 + 8 * (r >> 2) + (r & 3) < left ? s[i][r] : kNegInf;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 0; i < KB / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
+    top *= scale2;
+    if (__any(top > m + kSlack)) {
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float next = fmaxf(m, top);
+      const float f = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] *= f;
+    }
+    const float base = m == kNegInf ? 0.0f : -m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < KB / 16; ++u) {
+      uint32_t pw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = (u & 1) * 8 + 2 * i;
+        const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u >> 1][r], scale2, base));
+        const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u >> 1][r + 1], scale2, base));
+        sum += p0 + p1;
+        pw[i] = pack_bf16(p0, p1);
+      }
+      pb[u] = __builtin_bit_cast(v8bf, make_uint4(pw[0], pw[1], pw[2], pw[3]));
+    }
+    l += sum;
+    // P is made here and not, as the compiler would have it, where the next
+    // phase's products first need it
+#pragma unroll
+    for (int u = 0; u < KB / 16; ++u) asm volatile("" : "+v"(pb[u]));
   };
 
-  attend(false);
-  bool odd = false;
+  // Phases.  A wave alternates between matrix products (the scores of tile t
+  // and the values of tile t - 1) and the softmax of tile t; the second half
+  // of the waves is one phase behind the first, so that on every SIMD one wave
+  // multiplies while the other takes exponentials.  A barrier ends each phase.
+  // Before barrier 2 t (first half: before the products of tile t; second
+  // half: before the softmax of tile t - 1) every wave's loads of tile t have
+  // arrived; after it the last reader of tile t - 2 (the second half's
+  // products of tile t - 1) is done, and its buffer takes tile t + kBufs - 2.
+  const bool late = wave >= S::kWaves / 2;
+  auto even = [&](int t) {
+    if (t + S::kAhead <= tiles) wait_loads<(S::kAhead - 1) * S::kLoads>();
+    else wait_loads<0>();
+    barrier();
+    if (t + S::kAhead < tiles) fetch(t + S::kAhead);
+  };
+  m = kNegInf;
+  l = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) odd |= !(fabsf(o[i][r]) < __builtin_inff());
-  if (__syncthreads_or(odd)) attend(true);
+    for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < S::kAhead; ++t)
+    if (t < tiles) fetch(t);
+  auto before_softmax = [&](int t) {
+    if (late) even(t + 1);
+    else barrier();
+  };
+  auto after_softmax = [&](int t) {
+    if (late) barrier();
+    else even(t + 1);
+  };
+  even(0);
+  if (late) barrier();
+  if (mine > 0) {
+    multiply(0, std::true_type{}, std::false_type{});
+#pragma clang loop unroll(disable)
+    for (int t = 0; t < mine - 1; ++t) {
+      before_softmax(t);
+      softmax(t);
+      after_softmax(t);
+      multiply(t + 1, std::true_type{}, std::true_type{});
+    }
+    before_softmax(mine - 1);
+    softmax(mine - 1);
+    after_softmax(mine - 1);
+    multiply(mine, std::false_type{}, std::true_type{});
+  }
+#pragma clang loop unroll(disable)
+  for (int t = mine; t < tiles; ++t) {
+    before_softmax(t);
+    after_softmax(t);
+  }
+  if (!late) barrier();                                // the second half's last products
 
+  float odd = 0.0f;                                    // NaN as soon as one value is not finite
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) odd = fmaf(o[i][r], 0.0f, odd);
   l += __shfl_xor(l, 32);
   // a row without a score has the sum 0, one whose scores are all NaN the sum
   // NaN and the maximum -inf
@@ -337,39 +513,48 @@ __global__ __launch_bounds__(kThreads, D <= 192 ? 2 : 1) void prompt_attention_k
       }
     if (a.lse && g == 0) a.lse[(int64_t)(q0 + row) * a.NHq + h] = (m + __log2f(l)) * kLn2;
   }
+  if (__any(odd != 0.0f) && mine > 0) {
+    mend_rows<D>(a, q0 + row0, min(kRows, nq - row0), h, k0, nk, min(nk, mine * KB),
+                 a.causal ? row0 + 1 + nk - nq : nk, a.causal);
+  }
 }
 
-template <int D>
+template <typename S>
 hipError_t prepare_one() {
-  return prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<D>), lds_bytes<D>());
+  return prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<S>), S::kLds);
 }
 
-template <int D>
-void launch_one(const PromptArgs& p, int slots, int per_xcd, hipStream_t stream) {
-  prompt_attention_kernel<D><<<dim3((unsigned)(8 * per_xcd)), dim3(kThreads), lds_bytes<D>(), stream>>>(
-      p, slots, per_xcd);
+template <typename S>
+void launch_one(const PromptArgs& p, hipStream_t stream) {
+  // Each sequence ends with at most one part tile; one slot more, so that some
+  // slot is left for the rows behind the last sequence.
+  const int64_t slots = p.Tq / S::kBlockRows + p.B + (p.zero_tail ? 1 : 0);
+  const int64_t per_xcd = (slots * p.NHq + 7) / 8;
+  prompt_attention_kernel<S><<<dim3((unsigned)(8 * per_xcd)), dim3(S::kThreads), S::kLds, stream>>>(
+      p, (int)slots, (int)per_xcd);
 }
+
+typedef Shape<64, 8, 4> S64;
+typedef Shape<128, 8, 4> S128;
+typedef Shape<192, 8, 4> S192;
+typedef Shape<256, 8, 4> S256;
 
 }  // namespace
 
 hipError_t prepare_prompt_kernels() {
-  hipError_t e = prepare_one<64>();
-  if (e == hipSuccess) e = prepare_one<128>();
-  if (e == hipSuccess) e = prepare_one<192>();
-  if (e == hipSuccess) e = prepare_one<256>();
+  hipError_t e = prepare_one<S64>();
+  if (e == hipSuccess) e = prepare_one<S128>();
+  if (e == hipSuccess) e = prepare_one<S192>();
+  if (e == hipSuccess) e = prepare_one<S256>();
   return e;
 }
 
 hipError_t launch_prompt_attention(const PromptArgs& p, hipStream_t stream) {
-  // Each sequence ends with at most one part tile; one slot more, so that some
-  // slot is left for the rows behind the last sequence.
-  const int64_t slots = p.Tq / kBlockRows + p.B + (p.zero_tail ? 1 : 0);
-  const int64_t per_xcd = (slots * p.NHq + 7) / 8;
   switch (p.D) {
-    case 64: launch_one<64>(p, (int)slots, (int)per_xcd, stream); break;
-    case 128: launch_one<128>(p, (int)slots, (int)per_xcd, stream); break;
-    case 192: launch_one<192>(p, (int)slots, (int)per_xcd, stream); break;
-    default: launch_one<256>(p, (int)slots, (int)per_xcd, stream); break;
+    case 64: launch_one<S64>(p, stream); break;
+    case 128: launch_one<S128>(p, stream); break;
+    case 192: launch_one<S192>(p, stream); break;
+    default: launch_one<S256>(p, stream); break;
   }
   return hipGetLastError();
 }

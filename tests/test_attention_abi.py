@@ -124,6 +124,7 @@ def prompt(L, **kw):
     (dict(scale=float("nan")), UNSUP), (dict(Tq=(1 << 31) - 1), UNSUP), (dict(Tk=1 << 31), UNSUP),
     (dict(Tq=1 << 30, NHq=128, qs=16384, os=16384), UNSUP), (dict(qs=384), UNSUP),
     (dict(ks=250), UNSUP), (dict(vs=128), UNSUP), (dict(os=513), UNSUP), (dict(tail=4), UNSUP),
+    (dict(ks=(1 << 24) + 8), UNSUP), (dict(vs=1 << 30), UNSUP),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(cq=None), NULL),
     (dict(ck=None), NULL), (dict(out=None), NULL), (dict(q=P + 8), UNSUP), (dict(v=P + 2), UNSUP),
     (dict(Tq=0), OK), (dict(B=0), OK),

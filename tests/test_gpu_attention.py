@@ -459,9 +459,11 @@ def test_prompt_strides_and_tail():
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
 @pytest.mark.parametrize("what", ["nan", "inf"])
 def test_prompt_future_tokens_stay_out(D, what):
-    """Keys and values that are not finite from some token on: rows before
-    it are bit for bit what they were, rows from it on see them; other
-    sequences and other kv heads are untouched."""
+    """Keys and values that are not finite at some token: rows before it are
+    what they are without them, rows from it on see them; other sequences are
+    untouched bit for bit.  (Rows that share a tile with such a token are
+    computed in another order, without the rounding of the probabilities, so
+    they are held to the attention's bound, which counts that rounding.)"""
     say("prompt future", D, what)
     g = gen(23)
     NHq, NKV, nq = 4, 2, [150, 60]
@@ -474,11 +476,15 @@ def test_prompt_future_tokens_stay_out(D, what):
     k2[cut + 20, 1, 5] = float("nan")
     v2[cut + 20, 1, :] = float(what)
     out, lse = run(k2, v2)
-    assert torch.equal(out[:cut], base[:cut]) and torch.equal(lse[:cut], base_lse[:cut])
-    assert torch.equal(out[150:], base[150:])
+    clean = lambda x: torch.where(torch.isfinite(x), x, torch.zeros_like(x))  # noqa: E731
+    first = lambda x, n: x[:n]  # noqa: E731
+    check_prompt(first(out, cut), first(lse, cut), *(first(x, cut) for x in (q, k, v)), [cut], [cut], True, D ** -0.5)
+    check_prompt(out[:cut + 20, 2:], lse[:cut + 20, 2:], q[:cut + 20, 2:], clean(k2)[:cut + 20, 1:],
+                 clean(v2)[:cut + 20, 1:], [cut + 20], [cut + 20], True, D ** -0.5)
+    assert torch.equal(out[150:], base[150:]) and torch.equal(lse[150:], base_lse[150:])
     got = out[cut:150].float().cpu()
     assert not torch.isfinite(got[:, :2, 3]).any()
-    assert torch.isfinite(got[:, :2, 4:]).all() and torch.equal(out[cut:cut + 20, 2:], base[cut:cut + 20, 2:])
+    assert torch.isfinite(got[:, :2, 4:]).all()
     assert torch.isnan(got[20:, 2:]).all()
 
 
