@@ -432,7 +432,7 @@ moe_status moe_qk_norm_rope(const void* q, int64_t q_token_stride, const void* k
  *             V scales [4 quads][D / 32][4 tokens]
  *           (the order in which moe_cache4_attend's matrix operands take them)
  * Supported: D 64, 128, 192 or 256; page_size a multiple of 16, at most 4096;
- * NKV <= 65535; num_pages < 2^31.
+ * NKV <= 65535; num_pages * NKV * page_size / 16 < 2^31 tiles.
  */
 typedef struct {
   void* pages;

@@ -315,63 +315,66 @@ def inv_rope_fp8_quant_per_head(x, positions, cos_sin, R, interleaved=False, fmt
     return codes, scales
 
 
-def _heads(t, name, device=None, shape=None):
-    """The token stride of bfloat16 heads [T, heads, D] (token rows may be
-    strided, the heads of a token contiguous) on ``device``."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+# These calls are short (a decode step's kernels take 4 .. 40 us), so their
+# checks ask each tensor for little: about 0.1 us an attribute.
+
+def _heads(t, name, dev=None, shape=None):
+    """(T, heads, D, token stride) of bfloat16 heads [T, heads, D] (token rows
+    may be strided, the heads of a token contiguous) on device index ``dev``."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bfloat16 CUDA (HIP) tensor")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, D]")
     T, H, D = t.shape
-    if shape is not None and (T, H, D) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {[T, H, D]}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
     sT, sH, sD = t.stride()
     if D > 1 and sD != 1 or H > 1 and sH != D:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return sT if T > 1 else H * D
+    if shape is not None and shape != (T, H, D):
+        raise ValueError(f"{name} must be {list(shape)}, got {[T, H, D]}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+    return T, H, D, sT if T > 1 else H * D
 
 
-def _vector(t, dtype, n, name, device):
-    """The pointer of a contiguous [n] tensor on ``device``."""
-    p = _dev(t, dtype, name)
-    if tuple(t.shape) != (n,):
-        raise ValueError(f"{name} must be [{n}]")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return p
+def _vector(t, dtype, n, name, dev):
+    """The pointer of a contiguous [n] tensor on device index ``dev``."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor of {dtype}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be [{n}], contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+    return t.data_ptr()
 
 
-class _Launch:
-    """The stream of a call and, while entered, its device and stream as
-    torch's current ones: outputs and scratch made inside belong to that
-    stream, and inputs made on another stream are kept from reuse until the
-    call's work is done."""
+class _OnStream:
+    """Makes a call's device and stream torch's current ones for the time of
+    the call: outputs and scratch made inside belong to that stream, and
+    inputs of another stream are kept from reuse until the call's work is
+    done.  The usual call, on the current stream of the current device, needs
+    none of this (scope None)."""
 
-    def __init__(self, device, stream, inputs):
-        current = torch.cuda.current_stream(device)
-        self.other = stream is not None and stream != current
-        if self.other and stream.device != device:
-            raise ValueError(f"stream must be on {device}, got one on {stream.device}")
-        self.stream = stream if self.other else current
-        self.inputs = inputs
+    def __init__(self, dev, stream, inputs):
         self.scope = None
-        if self.other or torch.cuda.current_device() != device.index:
-            self.scope = torch.cuda.stream(self.stream)
+        if stream is None and torch._C._cuda_getDevice() == dev:
+            self.raw = torch._C._cuda_getCurrentRawStream(dev)
+            return
+        current = torch.cuda.current_stream(dev)
+        if stream is None:
+            stream = current
+        elif stream.device.index != dev:
+            raise ValueError(f"stream must be on device {dev}, got one on {stream.device}")
+        self.raw = stream.cuda_stream
+        if stream != current:
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+        self.scope = torch.cuda.stream(stream)
+        self.scope.__enter__()
 
-    def __enter__(self):
+    def done(self):
         if self.scope is not None:
-            self.scope.__enter__()
-            if self.other:
-                for t in self.inputs:
-                    if t is not None:
-                        t.record_stream(self.stream)
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def __exit__(self, *a):
-        if self.scope is not None:
-            self.scope.__exit__(*a)
+            self.scope.__exit__(None, None, None)
 
 
 def _no_overlap(out, inputs, name):
@@ -388,54 +391,66 @@ def _no_overlap(out, inputs, name):
             raise ValueError(f"{name} must not overlap an input")
 
 
+def _inner_out(y, x, shape, name, dev):
+    """The token stride of an output that may be its input itself."""
+    ys = _heads(y, name, dev, shape)[3]
+    if y.data_ptr() != x.data_ptr() or y.stride() != x.stride():
+        _no_overlap(y, (x,), name)
+    return ys
+
+
 def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=1e-6,
                  interleaved=False, q_out=None, k_out=None, stream=None):
     """(q_out, k_out) like bfloat16 query heads q [T, NHq, D] and key heads
     k [T, NHk, D] (or None): each head's RMS norm times its side's weight [D]
-    (bfloat16 or float32; None: no norm) and its rotary embedding at int64
-    ``positions`` [T] with the float32 table ``cos_sin`` [max_pos, R], in one
-    pass (moe_qk_norm_rope).  Token rows may be strided; ``q_out`` and
-    ``k_out`` may be q and k themselves."""
-    qs = _heads(q, "q")
-    T, NHq, D = q.shape
-    dev = q.device
-    NHk, ks = 0, 0
+    (bfloat16 or float32, both sides alike; None: no norm) and its rotary
+    embedding at int64 ``positions`` [T] with the float32 table ``cos_sin``
+    [max_pos, R], in one pass (moe_qk_norm_rope).  Token rows may be strided;
+    ``q_out`` and ``k_out`` may be q and k themselves, and must not overlap the
+    inputs otherwise."""
+    T, NHq, D, qs = _heads(q, "q")
+    dev = q.get_device()
+    NHk = ks = kos = 0
+    kp = kop = None
     if k is not None:
-        ks = _heads(k, "k", dev)
-        NHk = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != D:
+        Tk, NHk, Dk, ks = _heads(k, "k", dev)
+        if Tk != T or Dk != D:
             raise ValueError(f"k must be [{T}, heads, {D}]")
+        kp = k.data_ptr()
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out go with k")
     pp = _vector(positions, torch.int64, T, "positions", dev)
-    cp = _dev(cos_sin, torch.float32, "cos_sin")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != R or cos_sin.device != dev:
-        raise ValueError(f"cos_sin must be [max_pos, {R}] on {dev}")
-    wt = [w for w in (q_weight, k_weight) if w is not None]
-    f32 = bool(wt) and wt[0].dtype == torch.float32
-    for w in wt:
-        _vector(w, torch.float32 if f32 else torch.bfloat16, D, "weights", dev)
-    with _Launch(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out)) as st:
-        outs = []
-        for x, y, n in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-            if x is None:
-                outs.append((None, 0))
-                continue
-            if y is None:
-                y = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
-                outs.append((y, y.stride(0)))
-            else:
-                ys = _heads(y, n, dev, tuple(x.shape))
-                same = y.data_ptr() == x.data_ptr() and y.stride() == x.stride()
-                if not same:
-                    _no_overlap(y, [x], n)
-                outs.append((y, ys))
-        (qo, qos), (ko, kos) = outs
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype is not torch.float32 or not cos_sin.is_cuda:
+        raise TypeError("cos_sin must be a float32 CUDA (HIP) tensor")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != R or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
+        raise ValueError(f"cos_sin must be [max_pos, {R}], contiguous, on device {dev}")
+    w = q_weight if q_weight is not None else k_weight
+    f32, qw, kw = 0, None, None
+    if w is not None:
+        f32 = int(w.dtype is torch.float32)
+        wt = torch.float32 if f32 else torch.bfloat16
+        if q_weight is not None:
+            qw = _vector(q_weight, wt, D, "q_weight", dev)
+        if k_weight is not None:
+            kw = _vector(k_weight, wt, D, "k_weight", dev)
+    qos = NHq * D if q_out is None else _inner_out(q_out, q, (T, NHq, D), "q_out", dev)
+    if k is not None:
+        kos = NHk * D if k_out is None else _inner_out(k_out, k, (T, NHk, D), "k_out", dev)
+    on = _OnStream(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out))
+    try:
+        if q_out is None:
+            q_out = torch.empty_like(q)              # contiguous, whatever q's token stride
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty_like(k)
+            kop = k_out.data_ptr()
         _check(lib().moe_qk_norm_rope(
-            q.data_ptr(), qs, _ptr(k), ks, pp, cp, cos_sin.shape[0], T, NHq, NHk, D, R,
-            int(bool(interleaved)), _ptr(q_weight), _ptr(k_weight), int(f32), eps,
-            qo.data_ptr(), qos, _ptr(ko), kos, st), "moe_qk_norm_rope")
-    return qo, ko
+            q.data_ptr(), qs, kp, ks, pp, cos_sin.data_ptr(), cos_sin.shape[0], T, NHq, NHk, D, R,
+            1 if interleaved else 0, qw, kw, f32, eps, q_out.data_ptr(), qos, kop, kos, on.raw),
+            "moe_qk_norm_rope")
+    finally:
+        on.done()
+    return q_out, k_out
 
 
 class KVCache4:
@@ -451,8 +466,7 @@ class KVCache4:
     may run on any stream that is ordered after the writes they read."""
 
     def __init__(self, num_pages, page_size, NKV, D, device="cuda"):
-        nbytes = int(lib().moe_cache4_page_bytes(page_size, NKV, D))
-        if nbytes == 0:
+        if int(lib().moe_cache4_page_bytes(page_size, NKV, D)) == 0:
             raise MoEError(3, "moe_cache4_page_bytes")
         if num_pages <= 0:
             raise MoEError(2, "KVCache4")
@@ -467,36 +481,41 @@ class KVCache4:
         return self
 
     def _bind(self, pages):
-        p = _dev(pages, torch.uint8, "pages")
-        if pages.dim() != 4 or pages.shape[3] % 17:
-            raise ValueError("pages must be [num_pages, NKV, page_size / 16, 17 * D]")
+        if not isinstance(pages, torch.Tensor) or pages.dtype is not torch.uint8 or not pages.is_cuda:
+            raise TypeError("pages must be a uint8 CUDA (HIP) tensor")
+        if pages.dim() != 4 or pages.shape[3] % 17 or not pages.is_contiguous():
+            raise ValueError("pages must be [num_pages, NKV, page_size / 16, 17 * D], contiguous")
+        n, NKV, tiles, row = pages.shape
         self.pages = pages
-        self.num_pages, self.NKV, tiles, row = pages.shape
-        self.page_size, self.D = 16 * tiles, row // 17
-        self._c = Cache4(p, self.num_pages, self.page_size, self.NKV, self.D)
+        self.num_pages, self.NKV, self.page_size, self.D = n, NKV, 16 * tiles, row // 17
+        self._dev = pages.get_device()
+        self._c = ctypes.byref(Cache4(pages.data_ptr(), n, NKV=NKV, page_size=16 * tiles, D=row // 17))
 
-    def _table(self, block_table, B):
-        t = block_table
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+    def _table(self, t, B):
+        """(pointer, row stride, max_pages) of a block table."""
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda:
             raise TypeError("block_table must be an int32 CUDA (HIP) tensor")
-        if t.device != self.pages.device:
-            raise ValueError(f"block_table must be on {self.pages.device}")
-        if t.dim() != 2 or t.shape[0] != B or t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"block_table must be [{B}, max_pages], its rows contiguous")
-        return t.data_ptr(), max(t.stride(0), t.shape[1]) if B > 1 else t.shape[1], t.shape[1]
+        if t.dim() != 2 or t.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_pages]")
+        if t.get_device() != self._dev:
+            raise ValueError(f"block_table must be on device {self._dev}")
+        n = t.shape[1]
+        row, one = t.stride()
+        if n > 1 and one != 1:
+            raise ValueError("the rows of block_table must be contiguous")
+        return t.data_ptr(), row if B > 1 and row > n else n, n
 
     def _places(self, block_table, start, cu_seqlens, T):
-        dev = self.pages.device
         if start.dim() != 1:
             raise ValueError("start must be [B]")
-        B = start.shape[0]
+        B, dev = start.shape[0], self._dev
         sp = _vector(start, torch.int32, B, "start", dev)
-        if cu_seqlens is None:
-            if T != B:
-                raise ValueError(f"{T} tokens for {B} sequences need cu_seqlens")
+        if cu_seqlens is not None:
+            cu = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
+        elif T == B:
             cu = None
         else:
-            cu = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
+            raise ValueError(f"{T} tokens for {B} sequences need cu_seqlens")
         return (*self._table(block_table, B), sp, cu, B, T)
 
     def write(self, k, v, block_table, start, cu_seqlens=None, stream=None):
@@ -505,16 +524,17 @@ class KVCache4:
         token per sequence where cu_seqlens is None) goes to position
         start[b] + i.  Tokens without a place (a negative position, a position
         behind the table, a page id outside the cache) are skipped."""
-        dev = self.pages.device
-        ks = _heads(k, "k", dev)
-        shape = (k.shape[0], self.NKV, self.D)
-        if tuple(k.shape) != shape:
+        T, NKV, D, ks = _heads(k, "k", self._dev)
+        if NKV != self.NKV or D != self.D:
             raise ValueError(f"k must be [T, {self.NKV}, {self.D}]")
-        vs = _heads(v, "v", dev, shape)
-        at = self._places(block_table, start, cu_seqlens, shape[0])
-        with _Launch(dev, stream, (self.pages, k, v, block_table, start, cu_seqlens)) as st:
-            _check(lib().moe_cache4_write(ctypes.byref(self._c), k.data_ptr(), ks, v.data_ptr(), vs,
-                                          *at, st), "moe_cache4_write")
+        vs = _heads(v, "v", self._dev, (T, NKV, D))[3]
+        at = self._places(block_table, start, cu_seqlens, T)
+        on = _OnStream(self._dev, stream, (self.pages, k, v, block_table, start, cu_seqlens))
+        try:
+            _check(lib().moe_cache4_write(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at, on.raw),
+                   "moe_cache4_write")
+        finally:
+            on.done()
 
     def read(self, block_table, start, cu_seqlens, T, k=None, v=None, stream=None):
         """(k, v) bfloat16 [T, NKV, D]: the values that the cache holds of
@@ -522,19 +542,25 @@ class KVCache4:
         places that ``write`` would skip read as zeros.  Rows behind the last
         sequence are left as they were in a given k and v, and zero in new
         ones."""
-        dev = self.pages.device
         shape = (T, self.NKV, self.D)
         at = self._places(block_table, start, cu_seqlens, T)
         if (k is None) != (v is None):
             raise ValueError("give both k and v or neither")
         fresh = k is None
-        with _Launch(dev, stream, (self.pages, block_table, start, cu_seqlens, k, v)) as st:
+        ks = vs = self.NKV * self.D
+        if not fresh:
+            ks, vs = _heads(k, "k", self._dev, shape)[3], _heads(v, "v", self._dev, shape)[3]
+            _no_overlap(k, (self.pages, v), "k")
+            _no_overlap(v, (self.pages,), "v")
+        on = _OnStream(self._dev, stream, (self.pages, block_table, start, cu_seqlens, k, v))
+        try:
             if fresh:
-                k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-                v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-            ks, vs = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
-            _check(lib().moe_cache4_read(ctypes.byref(self._c), k.data_ptr(), ks, v.data_ptr(), vs,
-                                         *at, int(fresh), st), "moe_cache4_read")
+                k = self.pages.new_empty(shape, dtype=torch.bfloat16)
+                v = torch.empty_like(k)
+            _check(lib().moe_cache4_read(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at,
+                                         1 if fresh else 0, on.raw), "moe_cache4_read")
+        finally:
+            on.done()
         return k, v
 
     def attend(self, q, block_table, lens, scale=None, out=None, return_lse=False, stream=None):
@@ -544,28 +570,31 @@ class KVCache4:
         ``scale`` (default 1 / sqrt(D)).  With ``return_lse`` (out, lse), lse
         [B, NHq] float32 the logarithm of the sum of the exponentials.  A
         sequence without tokens gives zeros and -inf."""
-        dev = self.pages.device
-        qs = _heads(q, "q", dev)
-        B, NHq, D = q.shape
+        dev = self._dev
+        B, NHq, D, qs = _heads(q, "q", dev)
         if D != self.D:
             raise ValueError(f"q must be [B, heads, {self.D}]")
         lp = _vector(lens, torch.int32, B, "lens", dev)
         tp, ts, n = self._table(block_table, B)
+        os_ = NHq * D
+        if out is not None:
+            os_ = _heads(out, "out", dev, (B, NHq, D))[3]
+            _no_overlap(out, (q, self.pages), "out")
         L = lib()
-        with _Launch(dev, stream, (self.pages, q, block_table, lens, out)) as st:
+        nbytes = L.moe_cache4_attend_workspace_bytes(self._c, B, NHq, n)
+        on = _OnStream(dev, stream, (self.pages, q, block_table, lens, out))
+        try:
             if out is None:
-                out = torch.empty(B, NHq, D, dtype=torch.bfloat16, device=dev)
-                os_ = NHq * D
-            else:
-                os_ = _heads(out, "out", dev, (B, NHq, D))
-                _no_overlap(out, (q, self.pages), "out")
-            lse = torch.empty(B, NHq, dtype=torch.float32, device=dev) if return_lse else None
-            nbytes = int(L.moe_cache4_attend_workspace_bytes(ctypes.byref(self._c), B, NHq, n))
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+                out = torch.empty_like(q)
+            lse = q.new_empty((B, NHq), dtype=torch.float32) if return_lse else None
+            # scratch of this call alone: graphs that hold it may run side by side
+            ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
             _check(L.moe_cache4_attend(
-                ctypes.byref(self._c), q.data_ptr(), qs, tp, ts, n, lp, B, NHq,
-                D ** -0.5 if scale is None else scale, out.data_ptr(), os_, _ptr(lse), _ptr(ws),
-                nbytes, st), "moe_cache4_attend")
+                self._c, q.data_ptr(), qs, tp, ts, n, lp, B, NHq, D ** -0.5 if scale is None else scale,
+                out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
+                None if ws is None else ws.data_ptr(), nbytes, on.raw), "moe_cache4_attend")
+        finally:
+            on.done()
         return (out, lse) if return_lse else out
 
 
@@ -580,36 +609,37 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     float32.  A query that sees nothing gives zeros and -inf.  Rows behind the
     last sequence are left as they were in a given ``out``, zero in a new one
     and -inf in lse."""
-    qs = _heads(q, "q")
-    dev = q.device
-    Tq, NHq, D = q.shape
-    ks = _heads(k, "k", dev)
-    Tk, NKV, Dk = k.shape
+    Tq, NHq, D, qs = _heads(q, "q")
+    dev = q.get_device()
+    Tk, NKV, Dk, ks = _heads(k, "k", dev)
     if Dk != D:
         raise ValueError(f"k must be [Tk, heads, {D}]")
-    vs = _heads(v, "v", dev, (Tk, NKV, D))
+    vs = _heads(v, "v", dev, (Tk, NKV, D))[3]
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [B + 1]")
     B = cu_seqlens.shape[0] - 1
-    cq = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
-    if cu_seqlens_k is None:
-        if Tk != Tq:
-            raise ValueError("k has other rows than q: cu_seqlens_k is needed")
-        cu_seqlens_k = cu_seqlens
-    ck = _vector(cu_seqlens_k, torch.int32, B + 1, "cu_seqlens_k", dev)
+    cq = ck = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
+    if cu_seqlens_k is not None:
+        ck = _vector(cu_seqlens_k, torch.int32, B + 1, "cu_seqlens_k", dev)
+    elif Tk != Tq:
+        raise ValueError("k has other rows than q: cu_seqlens_k is needed")
     fresh = out is None
-    with _Launch(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out)) as st:
+    os_ = NHq * D
+    if not fresh:
+        os_ = _heads(out, "out", dev, (Tq, NHq, D))[3]
+        _no_overlap(out, (q, k, v), "out")
+    on = _OnStream(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out))
+    try:
         if fresh:
-            out = torch.empty(Tq, NHq, D, dtype=torch.bfloat16, device=dev)
-            os_ = NHq * D
-        else:
-            os_ = _heads(out, "out", dev, (Tq, NHq, D))
-            _no_overlap(out, (q, k, v), "out")
-        lse = torch.empty(Tq, NHq, dtype=torch.float32, device=dev) if return_lse else None
+            out = torch.empty_like(q)
+        lse = q.new_empty((Tq, NHq), dtype=torch.float32) if return_lse else None
         _check(lib().moe_prompt_attention(
             q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, B, Tq, Tk, NHq, NKV, D,
-            int(bool(causal)), D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-            _ptr(lse), 3 if fresh else 2, st), "moe_prompt_attention")
+            1 if causal else 0, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+            None if lse is None else lse.data_ptr(), 3 if fresh else 2, on.raw),
+            "moe_prompt_attention")
+    finally:
+        on.done()
     return (out, lse) if return_lse else out
 
 

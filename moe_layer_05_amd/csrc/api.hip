@@ -125,7 +125,9 @@ bool cache4_shape_ok(int page_size, int NKV, int D) {
 moe_status check_cache4(const moe_cache4* c) {
   if (!c) return MOE_ERR_NULL;
   if (c->num_pages <= 0 || c->page_size <= 0 || c->NKV <= 0 || c->D <= 0) return MOE_ERR_SHAPE;
-  if (!cache4_shape_ok(c->page_size, c->NKV, c->D) || c->num_pages >= ((int64_t)1 << 31))
+  // tiles are counted in 32 bits (2^31 of the smallest take 2.3 TB)
+  if (!cache4_shape_ok(c->page_size, c->NKV, c->D) || c->num_pages >= ((int64_t)1 << 31) ||
+      c->num_pages * c->NKV >= ((int64_t)1 << 31) / (c->page_size / 16))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -726,7 +728,8 @@ moe_status moe_cache4_read(const moe_cache4* cache, void* k, int64_t k_stride, v
 size_t moe_cache4_attend_workspace_bytes(const moe_cache4* cache, int32_t B, int32_t NHq,
                                          int32_t max_pages) {
   if (check_attend_shape(cache, B, NHq, max_pages) != MOE_OK || B == 0) return 0;
-  const int splits = cache4_attend_splits(B, NHq, cache->NKV, (int64_t)max_pages * cache->page_size);
+  const int splits = cache4_attend_splits(B, NHq, cache->NKV, cache->D,
+                                          (int64_t)max_pages * cache->page_size);
   return cache4_attend_workspace(B, NHq, cache->D, splits);
 }
 
@@ -744,7 +747,8 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_s
   if (B == 0) return MOE_OK;
   if (!cache->pages || !q || !lens || !out || (max_pages > 0 && !block_table)) return MOE_ERR_NULL;
   if (!aligned16(cache->pages) || !aligned16(q) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
-  const int splits = cache4_attend_splits(B, NHq, cache->NKV, (int64_t)max_pages * cache->page_size);
+  const int splits = cache4_attend_splits(B, NHq, cache->NKV, cache->D,
+                                          (int64_t)max_pages * cache->page_size);
   const size_t need = cache4_attend_workspace(B, NHq, cache->D, splits);
   if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   if (need && !aligned16(workspace)) return MOE_ERR_UNSUPPORTED;

@@ -5,10 +5,11 @@
 //   s_t = scale * q . k_t,  o = sum_t softmax(s)_t v_t,  lse = log sum_t e^{s_t}
 // in one pass with a running maximum m and sum l of each head in float32.
 //
-// HBM-bound: 17 * D / 16 bytes of cache per token and kv head against 4 * D
-// operations per query head, so up to 16 query heads share a column tile and
-// a wave has to keep up with the stream: per 32 tokens it reads four 16-byte
-// pieces per lane (K and V, D = 128) and issues about 200 instructions.
+// HBM-bound by its bytes: 17 * D / 16 of cache per token and kv head against
+// 4 * D operations per query head, so up to 16 query heads share a column
+// tile.  The stream leaves a compute unit 13 cycles a token (D = 128, 5.2
+// TB/s): per 32 tokens a wave reads four 16-byte pieces per lane and issues
+// about 270 instructions, which several waves per SIMD have to overlap.
 //
 // A wave takes steps of 32 tokens (two tiles of 16).  Both products run on
 // 16x16x32 bfloat16 matrix instructions; E2M1 times a power of two is exact
@@ -40,8 +41,15 @@
 // Work split: (kv head and column tile) x sequence x splits of the sequence.
 // A split takes an equal share of the sequence's own steps, worked out on the
 // device, so the host reads no lengths; the four waves of a workgroup
-// interleave the steps of its split and join in LDS.  With several splits the
-// partial sums go to scratch in float32 and a second launch joins them.
+// interleave the steps of its split and join in LDS.  A sequence that one
+// split holds is written at once; the partial sums of the others go to
+// scratch in float32 and a second launch joins them.  Page ids come 64 at a
+// time into a register, so that a step's loads wait for no other load.
+//
+// Measured (both launches): one sequence of 131072 tokens, 64 heads over 8 of
+// 128: 36 us = 3.9 TB/s of cache; 64 sequences of up to 8192, 32 heads over 4:
+// 43 us = 3.6 TB/s; 4 of up to 300, 16 over 2: 5.3 us.  Page ids loaded when a
+// step needed them: 60 us for the first.
 #include "cache4_device.hpp"
 
 namespace moe {
@@ -50,7 +58,10 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kStep = 32;                  // tokens of a wave's step
+constexpr int kMaxSplits = 128;
+constexpr int kOneSplit = 1024;            // tokens
 constexpr int kCols = 16;                  // query heads of a column tile
+constexpr int kLeast = 2 * kWaves;         // steps of a split, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;             // the maximum moves beyond this
@@ -86,9 +97,18 @@ __device__ __forceinline__ float final_factor(float top, float z) {
   return top == kNegInf ? z : 1.0f / z;
 }
 
-// First step of split s of n steps.
-__device__ __forceinline__ int split_begin(int n, int s, int splits) {
-  return (int)((int64_t)n * s / splits);
+// Steps of a split: an equal share of n steps, at least kLeast of them, so
+// that the splits with work come first; all of them where one split can.
+__device__ __forceinline__ int split_steps(int n, int splits) {
+  const int each = (n + splits - 1) / splits;
+  return each < kLeast ? kLeast : each;
+}
+__device__ __forceinline__ int sequence_steps(const AttendArgs& a, int b, int* len) {
+  const int64_t capacity = (int64_t)a.max_pages * a.c.page_tiles * kTileTokens;
+  int64_t n = a.lens[b];
+  n = n < 0 ? 0 : (n > capacity ? capacity : n);
+  *len = (int)n;
+  return (int)((n + kStep - 1) / kStep);
 }
 
 __device__ __forceinline__ v8bf as_bf8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -106,7 +126,7 @@ struct StepRegs {
   uint32_t ks64[2], vs64[2];
   bool there[2];                              // the tile is in the cache
 
-  __device__ __forceinline__ void load(const uint8_t* const (&tile)[2], int n, int g) {
+  __device__ __forceinline__ void fetch(const uint8_t* const (&tile)[2], int n, int g) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint8_t* t = tile[i];
@@ -138,6 +158,12 @@ __device__ __forceinline__ v8bf fp4_row8(uint32_t codes, float s) {
   return __builtin_bit_cast(v8bf, w);
 }
 
+// Byte i of a word as a scale of fp4_pair, which looks at the exponent bits
+// alone: the bits of the other bytes stay where they fall.
+__device__ __forceinline__ float byte_scale(uint32_t w, int i) {
+  return __uint_as_float(i == 3 ? w >> 1 : w << (23 - 8 * i));
+}
+
 // Tiles 2 * BYTE and 2 * BYTE + 1 of a chunk of V^T P^T: the operand rows are
 // the codes of byte BYTE of eight tokens' words.
 template <int BYTE>
@@ -157,11 +183,12 @@ __device__ __forceinline__ void v_tiles(const uint32_t (&w)[8], const float (&s)
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void cache4_attend_kernel(AttendArgs a) {
   constexpr int kWide = D / 128;
   constexpr bool kTail = D % 128 != 0;
   constexpr int kSteps = D / 32;             // matrix instructions of a score tile
   constexpr int kTiles = D / 16;             // row tiles of O^T
+  constexpr int kDeep = 2;                   // steps in registers
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n = lane & 15, g = lane >> 4;
@@ -169,14 +196,13 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
   const int kvh = blockIdx.y / a.col_tiles;
   const int col0 = (blockIdx.y - kvh * a.col_tiles) * kCols;   // first head of the tile in its group
   const int b = blockIdx.z;
-  const int64_t capacity = (int64_t)a.max_pages * a.c.page_tiles * kTileTokens;
-  int64_t len64 = a.lens[b];
-  len64 = len64 < 0 ? 0 : (len64 > capacity ? capacity : len64);
-  const int len = (int)len64;
-  const int nsteps = (len + kStep - 1) / kStep;
-  const int first = split_begin(nsteps, split, a.splits);
-  const int last = split_begin(nsteps, split + 1, a.splits);
-  if (first == last && a.splits > 1) return;   // the join passes over it
+  int len;
+  const int nsteps = sequence_steps(a, b, &len);
+  const int each = split_steps(nsteps, a.splits);
+  const int first = split * each;
+  const int last = min(nsteps, first + each);
+  if (first >= last && split > 0) return;
+  const bool alone = nsteps <= each;           // the whole sequence is here: no join
 
   const int head = col0 + n;                   // in the group
   const bool mine = head < a.G;
@@ -196,18 +222,33 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
     }
   }
 
+  // Page ids, 64 columns of the table in a register from column page0 on: the
+  // loads of a step wait for no other load.
   const int32_t* table = a.table + b * a.table_stride;
   const int tiles = (len + kTileTokens - 1) / kTileTokens;
-  auto locate = [&](int step, StepRegs<D>& r, const uint8_t* (&tile)[2]) {
+  auto column_of = [&](int tl) {
+    return (int)(a.page_magic ? __umulhi((uint32_t)tl, a.page_magic) : (uint32_t)tl);
+  };
+  int page0 = 0, pages = -1;
+  auto take_pages = [&](int col) {
+    page0 = col;
+    pages = col + lane < a.max_pages ? table[col + lane] : -1;
+  };
+  auto load = [&](int step, StepRegs<D>& r) {
+    if (step >= last) return;
+    if (column_of(min(2 * step + 1, tiles - 1)) >= page0 + kWave) take_pages(column_of(2 * step));
+    const uint8_t* tile[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int tl = 2 * step + i;
-      const uint32_t col = a.page_magic ? __umulhi((uint32_t)tl, a.page_magic) : (uint32_t)tl;
-      const int page = tl < tiles ? table[col] : -1;
-      r.there[i] = page >= 0 && page < a.c.num_pages;
-      tile[i] = cache4_tile(a.c, r.there[i] ? page : 0, kvh,
-                            r.there[i] ? tl - (int)col * a.c.page_tiles : 0);
+      const int col = column_of(tl);
+      const int page = tl < tiles ? __builtin_amdgcn_readlane(pages, col - page0) : -1;
+      r.there[i] = (uint32_t)page < (uint32_t)a.c.num_pages;
+      // a page that is not there is read as the cache's first tile
+      const uint32_t at = ((uint32_t)page * a.c.NKV + kvh) * a.c.page_tiles + (tl - col * a.c.page_tiles);
+      tile[i] = a.c.pages + (uint64_t)(r.there[i] ? at : 0u) * (uint32_t)cache4_tile_bytes(D);
     }
+    r.fetch(tile, n, g);
   };
 
   float m = kNegInf, l = 0.0f;                 // l: this lane's tokens only
@@ -237,21 +278,17 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
       sc[i] = acc;
     }
     float x[8];
-    uint32_t dead = 0;                         // tokens without a score
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3] * a.scale2;
-    if (!(r.there[0] && r.there[1] && (step + 1) * kStep <= len)) {   // wave-uniform
+    for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3];
+    const bool whole = r.there[0] && r.there[1] && (step + 1) * kStep <= len;   // uniform
+    const int left = len - step * kStep - 4 * g;       // of this lane's tokens, from the first on
+    auto dead = [&](int i) { return !r.there[i >> 2] || (i >> 2) * kTileTokens + (i & 3) >= left; };
+    if (!whole) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = step * kStep + (i >> 2) * kTileTokens + 4 * g + (i & 3);
-        if (!r.there[i >> 2] || t >= len) {
-          x[i] = kNegInf;
-          dead |= 1u << i;
-        }
-      }
+      for (int i = 0; i < 8; ++i) x[i] = dead(i) ? kNegInf : x[i];
     }
     float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                      fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                      fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * a.scale2;
     if (__any(top > m + kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -262,24 +299,20 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) o[i] *= f;
     }
-    const float base = m == kNegInf ? 0.0f : m;
+    const float base = m == kNegInf ? 0.0f : -m;
     float p[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(x[i] - base);
+    for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale2, base));
     l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     const v8bf pb = as_bf8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
                            pack_bf16(p[6], p[7]));
     // values
     auto scales = [&](uint32_t a0, uint32_t a1, float (&s)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w = i < 4 ? a0 : a1;
-        s[i] = cache4_scale((w >> (8 * (i & 3))) & 255u);
-      }
-      if (dead) {
+      for (int i = 0; i < 8; ++i) s[i] = byte_scale(i < 4 ? a0 : a1, i & 3);
+      if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (dead >> i & 1) s[i] = 1.0f;
+        for (int i = 0; i < 8; ++i) s[i] = dead(i) ? 1.0f : s[i];
       }
     };
 #pragma unroll
@@ -304,20 +337,25 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
     }
   };
 
-  StepRegs<D> cur, nxt;
-  const uint8_t* tile[2];
+  // kDeep steps in registers: the loads of the next ones are under way while
+  // one is worked on
+  StepRegs<D> r[kDeep];
   int step = first + wave;
   if (step < last) {
-    locate(step, cur, tile);
-    cur.load(tile, n, g);
-    for (; step < last; step += kWaves) {
-      const bool more = step + kWaves < last;
-      if (more) {
-        locate(step + kWaves, nxt, tile);
-        nxt.load(tile, n, g);
+    take_pages(column_of(2 * step));
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) load(step + i * kWaves, r[i]);
+#pragma clang loop unroll(disable)
+    while (true) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        if (step + i * kWaves < last) {
+          compute(r[i], step + i * kWaves);
+          load(step + (i + kDeep) * kWaves, r[i]);
+        }
       }
-      compute(cur, step);
-      cur = nxt;
+      step += kDeep * kWaves;
+      if (step >= last) break;
     }
   }
   l += __shfl_xor(l, 16);
@@ -360,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
       sum.x += f * v.x; sum.y += f * v.y; sum.z += f * v.z; sum.w += f * v.w;
     }
     const int h = kvh * a.G + col0 + col;
-    if (a.splits > 1) {
+    if (!alone) {
       const int64_t at = ((int64_t)b * a.NHq + h) * a.splits + split;
       *reinterpret_cast<float4*>(a.part_o + at * D + d) = sum;
       if (d == 0) a.part_ml[at] = make_float2(top, z);
@@ -376,62 +414,60 @@ __global__ __launch_bounds__(kThreads) void cache4_attend_kernel(AttendArgs a) {
   }
 }
 
-// Joins the splits of one head: a wave per (sequence, head), lanes over the
-// splits for the factors, then over the features.
+// Joins the splits of one head: a workgroup per (sequence, head), a lane for
+// every D / 64 features, the waves taking turns at the splits.  Sequences that
+// one split held are there already.
 template <int D>
 __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttendArgs a) {
   constexpr int kPer = D / kWave;              // features of a lane
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t row = (int64_t)blockIdx.x * kWaves + wave;     // b * NHq + h
-  if (row >= (int64_t)a.B * a.NHq) return;
+  const int64_t row = blockIdx.x;              // b * NHq + h
   const int b = (int)(row / a.NHq), h = (int)(row - (int64_t)b * a.NHq);
-  const int64_t capacity = (int64_t)a.max_pages * a.c.page_tiles * kTileTokens;
-  int64_t len = a.lens[b];
-  len = len < 0 ? 0 : (len > capacity ? capacity : len);
-  const int nsteps = (int)((len + kStep - 1) / kStep);
+  int len;
+  const int nsteps = sequence_steps(a, b, &len);
+  const int each = split_steps(nsteps, a.splits);
+  if (nsteps <= each) return;
+  const int parts = (nsteps + each - 1) / each;   // at most kMaxSplits
   const float2* ml = a.part_ml + row * a.splits;
-  const float* po = a.part_o + row * a.splits * D + lane * kPer;
-  float top = kNegInf;
-  for (int s = lane; s < a.splits; s += kWave)
-    if (split_begin(nsteps, s, a.splits) != split_begin(nsteps, s + 1, a.splits))
-      top = fmaxf(top, ml[s].x);
+  // factors of the parts: lane s of register i has that of part 64 i + s
+  float2 v[kMaxSplits / kWave];
+  float f[kMaxSplits / kWave], top = kNegInf, z = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kWave; ++i) {
+    v[i] = i * kWave + lane < parts ? ml[i * kWave + lane] : make_float2(kNegInf, 0.0f);
+    top = fmaxf(top, v[i].x);
+  }
   top = wave_max(top);
-  float z = 0.0f, acc[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-  for (int s0 = 0; s0 < a.splits; s0 += kWave) {
-    float f = 0.0f;
-    const int s = s0 + lane;
-    if (s < a.splits && split_begin(nsteps, s, a.splits) != split_begin(nsteps, s + 1, a.splits)) {
-      const float2 v = ml[s];
-      f = join_factor(v, top);
-      z += f * v.y;
-    }
-    const int end = min(kWave, a.splits - s0);
-    for (int i = 0; i < end; ++i) {
-      const float fi = __shfl(f, i);
-      // a split without work, or without a token in the cache, has f == 0
-      // and may hold anything
-      const float* src = po + (int64_t)(s0 + i) * D;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] += fi != 0.0f ? fi * src[k] : 0.0f;
-    }
+  for (int i = 0; i < kMaxSplits / kWave; ++i) {
+    f[i] = join_factor(v[i], top);
+    z += f[i] * v[i].y;
   }
   z = wave_sum(z);
-  const float f = final_factor(top, z);
-  uint16_t* out = a.out + b * a.out_stride + (int64_t)h * D + lane * kPer;
-  if constexpr (kPer == 1) {
-    *out = (uint16_t)pack_bf16(acc[0] * f, 0.0f);
-  } else if constexpr (kPer == 3) {
+  float acc[kPer];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) out[k] = (uint16_t)pack_bf16(acc[k] * f, 0.0f);
-  } else {
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
+  const float* po = a.part_o + row * a.splits * D + lane * kPer;
+#pragma unroll 8
+  for (int s = wave; s < parts; s += kWaves) {
+    const float fs = __shfl(s < kWave ? f[0] : f[1], s & (kWave - 1));
 #pragma unroll
-    for (int k = 0; k < kPer; k += 2)
-      *reinterpret_cast<uint32_t*>(out + k) = pack_bf16(acc[k] * f, acc[k + 1] * f);
+    for (int k = 0; k < kPer; ++k) acc[k] += fs * po[(int64_t)s * D + k];
   }
-  if (lane == 0 && a.lse) a.lse[row] = (top + __log2f(z)) * kLn2;
+  __shared__ float sum[kWaves][D];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) sum[wave][lane * kPer + k] = acc[k];
+  __syncthreads();
+  const float scale = final_factor(top, z);
+  const int d = threadIdx.x;
+  if (d < D) {
+    float o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) o += sum[w][d];
+    (a.out + b * a.out_stride + (int64_t)h * D)[d] = (uint16_t)pack_bf16(o * scale, 0.0f);
+  }
+  if (d == 0 && a.lse) a.lse[row] = (top + __log2f(z)) * kLn2;
 }
 
 int attend_lds(int D, int cols) { return kWaves * cols * (D + 4) * (int)sizeof(float); }
@@ -449,8 +485,7 @@ void launch_one(const AttendArgs& a, hipStream_t stream) {
   cache4_attend_kernel<D><<<grid, dim3(kThreads), attend_lds(D, a.G < kCols ? a.G : kCols),
                             stream>>>(a);
   if (a.splits > 1) {
-    const int64_t rows = (int64_t)a.B * a.NHq;
-    cache4_join_kernel<D><<<dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(a);
+    cache4_join_kernel<D><<<dim3((unsigned)(a.B * a.NHq)), dim3(kThreads), 0, stream>>>(a);
   }
 }
 
@@ -464,15 +499,23 @@ hipError_t prepare_cache4_attend_kernels() {
   return e;
 }
 
-// Splits of every sequence: enough workgroups for four on each of 256
-// compute units, each with at least one step of each of its waves when the
-// sequences are as long as the table allows.
-int cache4_attend_splits(int64_t B, int NHq, int NKV, int64_t capacity) {
+// Splits that a sequence may have.  Few sequences: as many as make one round
+// of resident workgroups (256 compute units, 4, 3 or 2 workgroups each by the
+// registers of the head size; one sequence of 131072 tokens, 8 kv heads of
+// 128: 96 splits 36 us, 128 splits, a round and a third, 42 us).  Sixteen and
+// more: their lengths differ, and shorter splits even them out (64 sequences
+// of up to 8192, 4 kv heads: 3 splits 48 us, 6 splits 43 us).  At most as many
+// as have kLeast steps each when the sequences are as long as the table
+// allows; one, and one launch, for tables of up to kOneSplit tokens (4
+// sequences of up to 300 tokens: 5.3 us against 7.4 us with a second launch).
+int cache4_attend_splits(int64_t B, int NHq, int NKV, int D, int64_t capacity) {
   const int64_t units = B * NKV * ((NHq / NKV + kCols - 1) / kCols);
-  int64_t s = (1024 + units - 1) / units;
-  const int64_t most = capacity / (kWaves * kStep);
+  const int64_t round = 256 * (D == 64 ? 4 : (D == 128 ? 3 : 2));
+  int64_t s = B < 16 ? round / units : (2 * round + units - 1) / units;
+  const int64_t most = capacity / (kLeast * kStep);
   if (s > most) s = most;
-  return (int)(s < 1 ? 1 : (s > 128 ? 128 : s));
+  if (capacity <= kOneSplit) s = 1;
+  return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
 
 size_t cache4_attend_workspace(int64_t B, int NHq, int D, int splits) {

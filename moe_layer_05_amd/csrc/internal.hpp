@@ -185,7 +185,7 @@ hipError_t launch_cache4_read(const Cache4& c, const CachePlaces& at, void* k, i
 
 // One query token per sequence over the cache.  splits > 1 needs
 // cache4_attend_workspace(...) bytes of scratch.
-int cache4_attend_splits(int64_t B, int NHq, int NKV, int64_t capacity);
+int cache4_attend_splits(int64_t B, int NHq, int NKV, int D, int64_t capacity);
 size_t cache4_attend_workspace(int64_t B, int NHq, int D, int splits);
 hipError_t launch_cache4_attend(const Cache4& c, const void* q, int64_t q_stride,
                                 const int32_t* table, int64_t table_stride, int max_pages,
