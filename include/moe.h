@@ -511,16 +511,22 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_t
  *   lse           [Tq][NHq] float32 (out), or NULL
  *   zero_tail     bit 0: rows of out behind the last sequence become 0, bit 1:
  *                 rows of lse behind it become -inf
+ *   workspace     >= moe_prompt_attention_workspace_bytes(...) device bytes,
+ *                 16-byte aligned; NULL where that is 0.  Calls that may
+ *                 overlap, graphs included, need workspaces of their own.
  * Supported: D 64, 128, 192 or 256; NHq a multiple of NKV; scale positive and
- * finite; k and v token strides <= 2^24; Tq, Tk < 2^31 - 2^16; (Tq / 32 + B) * NHq < 2^31.
+ * finite; k and v token strides <= 2^24; Tq * NHq and Tk < 2^31 - 2^16;
+ * (B + 8) * NKV < 2^29.
  */
+size_t moe_prompt_attention_workspace_bytes(int32_t B, int64_t Tq, int64_t Tk, int32_t NHq,
+                                            int32_t NKV, int32_t D);
 moe_status moe_prompt_attention(const void* q, int64_t q_token_stride, const void* k,
                                 int64_t k_token_stride, const void* v, int64_t v_token_stride,
                                 const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                                 int32_t B, int64_t Tq, int64_t Tk, int32_t NHq, int32_t NKV,
                                 int32_t D, int32_t causal, float scale, void* out,
                                 int64_t out_token_stride, float* lse, int32_t zero_tail,
-                                hipStream_t stream);
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

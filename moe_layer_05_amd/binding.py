@@ -160,7 +160,10 @@ _SIGS = {
         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
         ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
-        ctypes.c_void_p]),
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_prompt_attention_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+        ctypes.c_int32]),
 }
 
 # Stage boundaries of moe_fused_forward_timed (moe_stage in include/moe.h).
@@ -628,16 +631,20 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     if not fresh:
         os_ = _heads(out, "out", dev, (Tq, NHq, D))[3]
         _no_overlap(out, (q, k, v), "out")
+    L = lib()
+    nbytes = L.moe_prompt_attention_workspace_bytes(B, Tq, Tk, NHq, NKV, D)
     on = _OnStream(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out))
     try:
         if fresh:
             out = torch.empty_like(q)
         lse = q.new_empty((Tq, NHq), dtype=torch.float32) if return_lse else None
-        _check(lib().moe_prompt_attention(
+        # scratch of this call alone: graphs that hold it may run side by side
+        ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
+        _check(L.moe_prompt_attention(
             q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, B, Tq, Tk, NHq, NKV, D,
             1 if causal else 0, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-            None if lse is None else lse.data_ptr(), 3 if fresh else 2, on.raw),
-            "moe_prompt_attention")
+            None if lse is None else lse.data_ptr(), 3 if fresh else 2,
+            None if ws is None else ws.data_ptr(), nbytes, on.raw), "moe_prompt_attention")
     finally:
         on.done()
     return (out, lse) if return_lse else out

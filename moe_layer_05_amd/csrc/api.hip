@@ -161,6 +161,16 @@ moe_status check_attend_shape(const moe_cache4* c, int32_t B, int32_t NHq, int32
   return MOE_OK;
 }
 
+moe_status check_prompt_shape(int32_t B, int64_t Tq, int64_t Tk, int32_t NHq, int32_t NKV, int32_t D) {
+  if (B < 0 || Tq < 0 || Tk < 0 || NHq <= 0 || NKV <= 0 || D <= 0) return MOE_ERR_SHAPE;
+  if (NHq % NKV != 0) return MOE_ERR_SHAPE;
+  if (!head_size_ok(D)) return MOE_ERR_UNSUPPORTED;
+  // rows and workgroups are counted in 32 bits
+  const int64_t most = ((int64_t)1 << 31) - (1 << 16);
+  if (Tq >= most / NHq || Tk >= most || ((int64_t)B + 8) * NKV >= most / 4) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 bool block_m_ok(int bm) { return bm == 16 || bm == 32 || bm == 64 || bm == 128 || bm == 256; }
 
 // Upper bound of the number of blocks of the aligned layout: each active
@@ -758,18 +768,21 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_s
   });
 }
 
+size_t moe_prompt_attention_workspace_bytes(int32_t B, int64_t Tq, int64_t Tk, int32_t NHq,
+                                            int32_t NKV, int32_t D) {
+  if (check_prompt_shape(B, Tq, Tk, NHq, NKV, D) != MOE_OK) return 0;
+  return prompt_workspace(Tq, NHq, D, prompt_splits(Tq, Tk, B, NHq, NKV, D));
+}
+
 moe_status moe_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                 const void* v, int64_t v_stride, const int32_t* cu_q,
                                 const int32_t* cu_k, int32_t B, int64_t Tq, int64_t Tk,
                                 int32_t NHq, int32_t NKV, int32_t D, int32_t causal, float scale,
                                 void* out, int64_t out_stride, float* lse, int32_t zero_tail,
-                                hipStream_t stream) {
-  if (B < 0 || Tq < 0 || Tk < 0 || NHq <= 0 || NKV <= 0 || D <= 0) return MOE_ERR_SHAPE;
-  if (NHq % NKV != 0) return MOE_ERR_SHAPE;
-  if (!head_size_ok(D) || !scale_ok(scale) || (zero_tail & ~3)) return MOE_ERR_UNSUPPORTED;
-  const int64_t most = ((int64_t)1 << 31) - (1 << 16);
-  if (Tq >= most || Tk >= most) return MOE_ERR_UNSUPPORTED;
-  if ((Tq / 32 + B + 8) * NHq >= most) return MOE_ERR_UNSUPPORTED;
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const moe_status st = check_prompt_shape(B, Tq, Tk, NHq, NKV, D);
+  if (st != MOE_OK) return st;
+  if (!scale_ok(scale) || (zero_tail & ~3)) return MOE_ERR_UNSUPPORTED;
   if (!stride_ok(q_stride, NHq, D) || !stride_ok(out_stride, NHq, D) ||
       !stride_ok(k_stride, NKV, D) || !stride_ok(v_stride, NKV, D))
     return MOE_ERR_UNSUPPORTED;
@@ -779,6 +792,10 @@ moe_status moe_prompt_attention(const void* q, int64_t q_stride, const void* k, 
   if (B == 0 && !zero_tail) return MOE_OK;
   if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v))) return MOE_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
+  const int splits = prompt_splits(Tq, Tk, B, NHq, NKV, D);
+  const size_t need = prompt_workspace(Tq, NHq, D, splits);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return MOE_ERR_UNSUPPORTED;
   return guarded([&] {
     PromptArgs p{};
     p.q = static_cast<const uint16_t*>(q);
@@ -801,7 +818,8 @@ moe_status moe_prompt_attention(const void* q, int64_t q_stride, const void* k, 
     p.causal = causal != 0;
     p.zero_tail = zero_tail;
     p.scale = scale;
-    return launch_prompt_attention(p, stream);
+    p.splits = splits;
+    return launch_prompt_attention(p, workspace, stream);
   });
 }
 

@@ -25,9 +25,9 @@
 //    The matching V operand is 8n .. 8n + 7 of the same tokens: one 16-byte
 //    load per tile; a conversion gives two features of one token, a byte
 //    permute pairs them by feature.
-// Probabilities are rounded to bfloat16 for the second product (relative
-// 2^-9 each, random over the tokens: the output's error stays at the size of
-// its own rounding); their sum is taken in float32 before that.
+// Probabilities enter the second product as two bfloat16, the second what the
+// first leaves (2^-16 relative): one alone would add as much error as the
+// output's own rounding, and the matrix unit has room beside the stream.
 //
 // The running maximum moves only when a score passes it by more than 8 (in
 // powers of two), so most steps skip the exchange between lanes and the
@@ -167,7 +167,7 @@ __device__ __forceinline__ float byte_scale(uint32_t w, int i) {
 // Tiles 2 * BYTE and 2 * BYTE + 1 of a chunk of V^T P^T: the operand rows are
 // the codes of byte BYTE of eight tokens' words.
 template <int BYTE>
-__device__ __forceinline__ void v_tiles(const uint32_t (&w)[8], const float (&s)[8], v8bf p,
+__device__ __forceinline__ void v_tiles(const uint32_t (&w)[8], const float (&s)[8], v8bf p, v8bf rest,
                                         v4f& even, v4f& odd) {
   uint32_t x[8];
 #pragma unroll
@@ -178,8 +178,11 @@ __device__ __forceinline__ void v_tiles(const uint32_t (&w)[8], const float (&s)
     e[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
     o[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
   }
-  even = mfma(as_bf8(e[0], e[1], e[2], e[3]), p, even);
-  odd = mfma(as_bf8(o[0], o[1], o[2], o[3]), p, odd);
+  const v8bf ev = as_bf8(e[0], e[1], e[2], e[3]), od = as_bf8(o[0], o[1], o[2], o[3]);
+  even = mfma(ev, p, even);
+  odd = mfma(od, p, odd);
+  even = mfma(ev, rest, even);
+  odd = mfma(od, rest, odd);
 }
 
 template <int D>
@@ -304,8 +307,13 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_attend_kernel(AttendArgs a
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale2, base));
     l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-    const v8bf pb = as_bf8(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                           pack_bf16(p[6], p[7]));
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+      lo[i] = pack_bf16(p[2 * i] - bf16_lo(hi[i]), p[2 * i + 1] - bf16_hi(hi[i]));
+    }
+    const v8bf pb = as_bf8(hi[0], hi[1], hi[2], hi[3]), pl = as_bf8(lo[0], lo[1], lo[2], lo[3]);
     // values
     auto scales = [&](uint32_t a0, uint32_t a1, float (&s)[8]) {
 #pragma unroll
@@ -321,10 +329,10 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_attend_kernel(AttendArgs a
       const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
       float s[8];
       scales(r.vs[0][c], r.vs[1][c], s);
-      v_tiles<0>(w, s, pb, o[8 * c], o[8 * c + 1]);
-      v_tiles<1>(w, s, pb, o[8 * c + 2], o[8 * c + 3]);
-      v_tiles<2>(w, s, pb, o[8 * c + 4], o[8 * c + 5]);
-      v_tiles<3>(w, s, pb, o[8 * c + 6], o[8 * c + 7]);
+      v_tiles<0>(w, s, pb, pl, o[8 * c], o[8 * c + 1]);
+      v_tiles<1>(w, s, pb, pl, o[8 * c + 2], o[8 * c + 3]);
+      v_tiles<2>(w, s, pb, pl, o[8 * c + 4], o[8 * c + 5]);
+      v_tiles<3>(w, s, pb, pl, o[8 * c + 6], o[8 * c + 7]);
     }
     if constexpr (kTail) {
       const uint2 &v0 = r.v64[0], &v1 = r.v64[1];
@@ -332,8 +340,8 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_attend_kernel(AttendArgs a
                              v1.x & 0xFFFFu, v1.x >> 16, v1.y & 0xFFFFu, v1.y >> 16};
       float s[8];
       scales(r.vs64[0], r.vs64[1], s);
-      v_tiles<0>(w, s, pb, o[8 * kWide], o[8 * kWide + 1]);
-      v_tiles<1>(w, s, pb, o[8 * kWide + 2], o[8 * kWide + 3]);
+      v_tiles<0>(w, s, pb, pl, o[8 * kWide], o[8 * kWide + 1]);
+      v_tiles<1>(w, s, pb, pl, o[8 * kWide + 2], o[8 * kWide + 3]);
     }
   };
 

@@ -203,8 +203,13 @@ struct PromptArgs {
   int B, NHq, NKV, D;
   int causal, zero_tail;
   float scale;
+  int splits;                  // of the keys; > 1 needs prompt_workspace(...) bytes of scratch
+  float* part_o;               // [Tq][NHq][splits][D]
+  float2* part_ml;             // [Tq][NHq][splits] (maximum in powers of two, sum)
 };
-hipError_t launch_prompt_attention(const PromptArgs& p, hipStream_t stream);
+int prompt_splits(int64_t Tq, int64_t Tk, int64_t B, int NHq, int NKV, int D);
+size_t prompt_workspace(int64_t Tq, int NHq, int D, int splits);
+hipError_t launch_prompt_attention(PromptArgs p, void* workspace, hipStream_t stream);
 
 // The shape is chosen for num_cus compute units (the current device's);
 // nblk_cap is the layout's block capacity, est_blocks the blocks a call

@@ -55,7 +55,10 @@
 namespace moe {
 namespace {
 
-constexpr int kRows = 32;                       // query rows of a wave
+constexpr int kRows = 32;                       // rows of a wave
+constexpr int kBlockRows = 256;                 // rows of a workgroup
+constexpr int kMaxSplits = 64;
+constexpr int kLeast = 4;                       // tiles of keys of a split, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
@@ -81,8 +84,10 @@ struct Shape {
   static_assert(2 * kHalf % (1024 * kWaves) == 0, "whole loads per wave");
   // operands read ahead, and whether the two products take turns: as far as
   // the registers go (D = 256 would spill)
-  static constexpr int kReadAhead = D <= 192 ? 4 : 2;
+  static constexpr int kReadAhead = D == 128 || D == 192 ? 4 : 2;
   static constexpr bool kTurns = D <= 192;
+  // D = 64: two workgroups to a compute unit
+  static constexpr int kWavesPerSimd = D == 64 ? 4 : 2;
   // The 16-byte pieces of a row are XOR-ed with a function of the row inside
   // groups of kGroup.  The 64 banks hold 256 bytes: rows of 256 or 512 bytes
   // all start at the same bank; 16 rows that read the same piece need 16
@@ -127,51 +132,93 @@ __device__ __forceinline__ void barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int ROWS>
-__device__ __forceinline__ int seq_tiles(const PromptArgs& p, int b, int* q0, int* q1) {
+// Where sequence b's queries start, and how many it has.
+__device__ __forceinline__ int query_span(const PromptArgs& p, int b, int* q0) {
   int64_t lo = p.cu_q[b], hi = p.cu_q[b + 1];
   lo = lo < 0 ? 0 : (lo > p.Tq ? p.Tq : lo);
   hi = hi < lo ? lo : (hi > p.Tq ? p.Tq : hi);
   *q0 = (int)lo;
-  *q1 = (int)hi;
-  return (int)((hi - lo + ROWS - 1) / ROWS);
+  return (int)(hi - lo);
+}
+__device__ __forceinline__ int key_span(const PromptArgs& p, int b, int64_t* k0) {
+  int64_t lo = p.cu_k[b], hi = p.cu_k[b + 1];
+  lo = lo < 0 ? 0 : (lo > p.Tk ? p.Tk : lo);
+  hi = hi < lo ? lo : (hi > p.Tk ? p.Tk : hi);
+  *k0 = lo;
+  return (int)(hi - lo);
+}
+// Keys that query i of nq sees.
+__device__ __forceinline__ int keys_seen(const PromptArgs& p, int i, int nq, int nk) {
+  if (!p.causal) return nk;
+  const int64_t l = (int64_t)i + 1 + nk - nq;
+  return l < 0 ? 0 : (l > nk ? nk : (int)l);
+}
+// Tiles of keys of a split, of n: an equal share, kLeast at least, so that the
+// splits with work come first.
+__device__ __forceinline__ int split_tiles(int n, int splits) {
+  const int each = (n + splits - 1) / splits;
+  return each < kLeast ? kLeast : each;
 }
 
-// Mends a wave's rows q_row .. + rows of head h after their last tile, when one
-// of them holds a value that is not finite.  Row i sees the keys j < lim(i) =
-// clamp(first_lim + i * causal, 0, nk), but its products ran over those up to
-// key_end, with probability 0: where a value in between is not finite,
-// 0 * NaN has reached rows that do not see it.  Those rows are computed again,
-// one lane holding D / 64 features, over exactly the keys they see.  Reached
-// by no finite values; kept out of line so that it costs the others no
-// register.
+// A finished row, or its part in a split: the sums of features d .. d + N - 1.
+template <int N>
+__device__ __forceinline__ void store_row(const PromptArgs& a, bool alone, int64_t token, int h, int split,
+                                          int d, const float (&o)[N], float m, float l, bool first) {
+  if (alone) {
+    // a row without a score has the sum 0, one whose scores are all NaN the
+    // sum NaN and the maximum -inf
+    const float f = m == kNegInf ? l : 1.0f / l;
+    uint16_t* dst = a.out + token * a.out_stride + (int64_t)h * a.D + d;
+    if constexpr (N == 4) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) dst[k] = (uint16_t)pack_bf16(o[k] * f, 0.0f);
+    }
+    if (first && a.lse) a.lse[token * a.NHq + h] = (m + __log2f(l)) * kLn2;
+  } else {
+    const int64_t at = (token * a.NHq + h) * a.splits + split;
+    if constexpr (N == 4) {
+      *reinterpret_cast<float4*>(a.part_o + at * a.D + d) = make_float4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) a.part_o[at * a.D + d + k] = o[k];
+    }
+    if (first) a.part_ml[at] = make_float2(m, l);
+  }
+}
+
+// Mends a wave's rows row0 .. + rows (row r is query r / G of the sequence and
+// head r % G of the group) after their last tile, when one of them holds a
+// value that is not finite.  A row's products ran over the keys key0 .. key1,
+// with probability 0 for those it does not see: where such a key's value is
+// not finite, 0 * NaN has reached it.  Those rows are computed again, a lane
+// holding D / 64 features, over exactly the keys they see.  Reached by no
+// finite values; kept out of line so that it costs the others no register.
 template <int D>
-__attribute__((noinline)) __device__ void mend_rows(PromptArgs a, int64_t q_row, int rows, int h, int64_t k0,
-                                                    int nk, int key_end, int first_lim, int causal) {
+__attribute__((noinline)) __device__ void mend_rows(PromptArgs a, int q0, int nq, int row0, int rows, int kvh,
+                                                    int64_t k0, int nk, int key0, int key1, bool alone, int split) {
   constexpr int kPer = D / kWave;
-  const int f0 = (threadIdx.x & (kWave - 1)) * kPer;
-  const int kvh = h / (a.NHq / a.NKV);
+  const int lane = threadIdx.x & (kWave - 1), f0 = lane * kPer;
+  const int G = a.NHq / a.NKV;
   const float scale2 = a.scale * kLog2e;
-  auto limit = [&](int i) {
-    const int l = first_lim + i * causal;
-    return l < 0 ? 0 : (l > nk ? nk : l);
-  };
   int bad = -1;                                        // the last key whose value is not finite
-  for (int j = limit(0); j < key_end; ++j) {
+  for (int j = max(key0, keys_seen(a, row0 / G, nq, nk)); j < key1; ++j) {
     bool odd = false;
     for (int d = 0; d < kPer; ++d)
       odd |= (a.v[(k0 + j) * a.v_stride + (int64_t)kvh * D + f0 + d] & 0x7F80u) == 0x7F80u;
     if (__any(odd)) bad = j;
   }
-  for (int i = 0; i < rows && limit(i) <= bad; ++i) {
-    const int64_t row = q_row + i;
-    const int lim = limit(i);
+  for (int r = row0; r < row0 + rows && keys_seen(a, r / G, nq, nk) <= bad; ++r) {
+    const int64_t token = q0 + r / G;
+    const int h = kvh * G + r % G;
+    const int lim = min(key1, keys_seen(a, r / G, nq, nk));
     float q[kPer], o[kPer], m = kNegInf, l = 0.0f;
     for (int d = 0; d < kPer; ++d) {
-      q[d] = bf16_lo(a.q[row * a.q_stride + (int64_t)h * D + f0 + d]);
+      q[d] = bf16_lo(a.q[token * a.q_stride + (int64_t)h * D + f0 + d]);
       o[d] = 0.0f;
     }
-    for (int j = 0; j < lim; ++j) {
+    for (int j = key0; j < lim; ++j) {
       const uint16_t* k = a.k + (k0 + j) * a.k_stride + (int64_t)kvh * D + f0;
       const uint16_t* v = a.v + (k0 + j) * a.v_stride + (int64_t)kvh * D + f0;
       float s = 0.0f;
@@ -184,35 +231,47 @@ __attribute__((noinline)) __device__ void mend_rows(PromptArgs a, int64_t q_row,
       l = l * f + p;
       for (int d = 0; d < kPer; ++d) o[d] = o[d] * f + p * bf16_lo(v[d]);
     }
-    const float f = m == kNegInf ? l : 1.0f / l;
-    for (int d = 0; d < kPer; ++d)
-      a.out[row * a.out_stride + (int64_t)h * D + f0 + d] = (uint16_t)pack_bf16(o[d] * f, 0.0f);
-    if (f0 == 0 && a.lse) a.lse[row * a.NHq + h] = (m + __log2f(l)) * kLn2;
+    store_row(a, alone, token, h, split, f0, o, m, l, lane == 0);
   }
 }
 
 template <typename S>
-__global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_kernel(
-    PromptArgs a, int slots, int per_xcd) {
+__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attention_kernel(
+    PromptArgs a, int slots) {
   constexpr int D = S::D, KB = S::KB;
-  constexpr int kPieces = D / 8;                      // 16-byte pieces of a row
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int g = lane >> 5, c = lane & 31;
+  const int G = a.NHq / a.NKV;
 
-  const int w = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if (w >= slots * a.NHq) return;
-  const int h = w / slots;
-  const int x = w - h * slots;
-  const int kvh = h / (a.NHq / a.NKV);
+  // Workgroup b runs on XCD b & 7.  With 1, 2, 4 or 8 kv heads (or a multiple
+  // of 8) each XCD keeps to one kv head at a time, so that its keys stay in
+  // that L2, and the XCDs of a head take its slots in turn: the slots with the
+  // most keys go first, on all XCDs alike.
+  int kvh, rest;
+  if (8 % a.NKV == 0) {
+    const int turn = blockIdx.x & 7;
+    kvh = turn % a.NKV;
+    rest = (blockIdx.x >> 3) * (8 / a.NKV) + turn / a.NKV;
+  } else if (a.NKV % 8 == 0) {
+    const int j = blockIdx.x >> 3, heads = a.NKV / 8;
+    rest = j / heads;
+    kvh = (j - rest * heads) * 8 + (blockIdx.x & 7);
+  } else {
+    rest = blockIdx.x / a.NKV;
+    kvh = blockIdx.x - rest * a.NKV;
+  }
+  const int x = rest / a.splits, split = rest - x * a.splits;
+  if (x >= slots) return;
 
   // the sequence and tile of slot x: a running sum of the sequences' tiles
-  int seq = -1, tile = 0, q0 = 0, q1 = 0, total = 0;
+  int seq = -1, tile = 0, q0 = 0, nq = 0, total = 0;
   for (int b0 = 0; b0 < a.B; b0 += kWave) {
-    int lo = 0, hi = 0;
-    const int nt = b0 + lane < a.B ? seq_tiles<S::kBlockRows>(a, b0 + lane, &lo, &hi) : 0;
+    int lo = 0;
+    const int n = b0 + lane < a.B ? query_span(a, b0 + lane, &lo) : 0;
+    const int nt = (n * G + S::kBlockRows - 1) / S::kBlockRows;
     const int incl = wave_inclusive_sum_dpp(nt);
     const unsigned long long hit = __ballot(x >= total + incl - nt && x < total + incl);
     if (hit) {
@@ -220,7 +279,7 @@ __global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_k
       seq = b0 + src;
       tile = __shfl(total + incl, src) - 1 - x;       // the last tile first
       q0 = __shfl(lo, src);
-      q1 = __shfl(hi, src);
+      nq = __shfl(n, src);
       break;
     }
     total += __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -228,39 +287,47 @@ __global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_k
   seq = __builtin_amdgcn_readfirstlane(seq);
   if (seq < 0) {
     // no tile: such slots share the rows behind the last sequence
-    if (!a.zero_tail) return;
+    if (split > 0) return;
     int64_t behind = a.cu_q[a.B];
     behind = behind < 0 ? 0 : behind;
     for (int64_t t = behind + (x - total); t < a.Tq; t += slots - total) {
-      if ((a.zero_tail & 1) && tid < kPieces)
-        reinterpret_cast<uint4*>(a.out + t * a.out_stride + (int64_t)h * D)[tid] = make_uint4(0, 0, 0, 0);
-      if ((a.zero_tail & 2) && tid == 0 && a.lse) a.lse[t * a.NHq + h] = kNegInf;
+      if (a.zero_tail & 1)
+        for (int i = tid; i < G * (D / 8); i += S::kThreads)
+          reinterpret_cast<uint4*>(a.out + t * a.out_stride + (int64_t)kvh * G * D)[i] = make_uint4(0, 0, 0, 0);
+      if ((a.zero_tail & 2) && a.lse)
+        for (int i = tid; i < G; i += S::kThreads) a.lse[t * a.NHq + kvh * G + i] = kNegInf;
     }
     return;
   }
   tile = __builtin_amdgcn_readfirstlane(tile);
   q0 = __builtin_amdgcn_readfirstlane(q0);
-  q1 = __builtin_amdgcn_readfirstlane(q1);
-  int64_t k0 = a.cu_k[seq], k1 = a.cu_k[seq + 1];
-  k0 = k0 < 0 ? 0 : (k0 > a.Tk ? a.Tk : k0);
-  k1 = k1 < k0 ? k0 : (k1 > a.Tk ? a.Tk : k1);
-  const int nq = q1 - q0, nk = (int)(k1 - k0);
-  // keys that in-sequence row i sees
-  auto limit = [&](int i) {
-    if (!a.causal) return nk;
-    const int64_t l = (int64_t)i + 1 + nk - nq;
-    return l < 0 ? 0 : (l > nk ? nk : (int)l);
-  };
+  nq = __builtin_amdgcn_readfirstlane(nq);
+  int64_t k0;
+  const int nk_all = key_span(a, seq, &k0);
+  const int nr = nq * G;                              // rows: (query, head of the group)
   const int block0 = tile * S::kBlockRows;
   const int row0 = block0 + wave * kRows;
-  const int row = row0 + c;                           // in the sequence; may be past its end
-  const int lim = limit(row);
-  const int wave_max = row0 < nq ? limit(min(row0 + kRows, nq) - 1) : 0;
-  const int tiles = (limit(min(block0 + S::kBlockRows, nq) - 1) + KB - 1) / KB;
+  const int last_row = min(block0 + S::kBlockRows, nr) - 1;
+  // this split's tiles of keys; from here on keys and limits count from its
+  // first key on
+  const int all_tiles = (keys_seen(a, last_row / G, nq, nk_all) + KB - 1) / KB;
+  const int each = split_tiles(all_tiles, a.splits);
+  const bool alone = all_tiles <= each;
+  const int tiles = min(all_tiles - split * each, each);
+  if (tiles <= 0 && split > 0) return;
+  const int key0 = split * each * KB;
+  const int nk = nk_all - key0;
+  auto limit = [&](int r) {                           // keys that row r sees here
+    const int l = keys_seen(a, r / G, nq, nk_all) - key0;
+    return l < 0 ? 0 : min(l, tiles * KB);
+  };
+  const int lim = limit(min(row0 + c, nr - 1));       // lanes past the end repeat the last row
+  const int wave_max = row0 < nr ? limit(min(row0 + kRows, nr) - 1) : 0;
 
   v8bf q[D / 16];
   {
-    const uint16_t* src = a.q + (int64_t)(q0 + min(row, nq - 1)) * a.q_stride + (int64_t)h * D + g * 8;
+    const int row = min(row0 + c, nr - 1);
+    const uint16_t* src = a.q + (int64_t)(q0 + row / G) * a.q_stride + (int64_t)(kvh * G + row % G) * D + g * 8;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
       q[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 16 * s));
@@ -270,35 +337,49 @@ __global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_k
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
   const float scale2 = a.scale * kLog2e;
-  const uint16_t* kbase = a.k + k0 * a.k_stride + (int64_t)kvh * D;
-  const uint16_t* vbase = a.v + k0 * a.v_stride + (int64_t)kvh * D;
+  const uint16_t* kbase = a.k + (k0 + key0) * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vbase = a.v + (k0 + key0) * a.v_stride + (int64_t)kvh * D;
 
   // This wave's loads of a tile: 1 KB pieces wave, wave + kWaves, .. of K's
   // and then V's LDS image; the lane brings the 16 bytes that belong there.
   const uint32_t lds0 = lds_addr(smem);
-  int lrow[S::kLoads];                                // row in the tile
-  uint32_t loff[S::kLoads];                           // byte offset of that row's piece
+  constexpr int kRowsOfLoad = 1024 / S::kRowBytes;    // (D = 192: not whole, kEven false)
+  // Where a wave's loads of K fall on whole rounds of the waves, they differ by
+  // whole rows that leave the XOR as it is: one offset does for all of them,
+  // and one for those of V.
+  constexpr bool kEven = S::kHalf / 1024 % S::kWaves == 0;
+  constexpr int kHalfLoads = S::kLoads / 2;
+  static_assert(!kEven || S::kWaves * kRowsOfLoad % 16 == 0, "rows of a round");
+  auto load_is_v = [&](int i) { return kEven ? i >= kHalfLoads : wave + i * S::kWaves >= S::kHalf / 1024; };
+  auto image_byte = [&](int i) {                      // of K or V
+    return (wave + i * S::kWaves) * 1024 + lane * 16 - (load_is_v(i) ? S::kHalf : 0);
+  };
+  uint32_t loff[kEven ? 2 : S::kLoads];               // byte offset of the row's piece
 #pragma unroll
-  for (int i = 0; i < S::kLoads; ++i) {
-    const int part = wave + i * S::kWaves;
-    const bool is_v = part >= S::kHalf / 1024;
-    const int byte = (part * 1024 + lane * 16) - (is_v ? S::kHalf : 0);
-    const int r = byte / S::kRowBytes, p = (byte - r * S::kRowBytes) / 16;
-    lrow[i] = r;
+  for (int i = 0; i < (kEven ? 2 : S::kLoads); ++i) {
+    const int l = kEven ? i * kHalfLoads : i;
+    const int r = image_byte(l) / S::kRowBytes, p = (image_byte(l) - r * S::kRowBytes) / 16;
     const int piece = (p & ~(S::kGroup - 1)) | ((p & (S::kGroup - 1)) ^ S::mix(r));
-    loff[i] = (uint32_t)r * (uint32_t)(2 * (is_v ? a.v_stride : a.k_stride)) + piece * 16;
+    loff[i] = (uint32_t)r * (uint32_t)(2 * (load_is_v(l) ? a.v_stride : a.k_stride)) + piece * 16;
   }
   auto fetch = [&](int t) {
-    const uint32_t buf = lds0 + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
-    const int over = t * KB + KB - nk;                // rows behind the end repeat the last one
+    const uint32_t buf = lds0 + (uint32_t)(t % S::kBufs) * (2 * S::kHalf) + wave * 1024;
+    const int last = nk - 1 - t * KB;                 // rows behind the last key repeat it
+    const bool whole_tile = last >= KB - 1;
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
-      const int part = wave + i * S::kWaves;
-      const bool is_v = part >= S::kHalf / 1024;
+      const bool is_v = load_is_v(i);
       const int64_t stride = is_v ? a.v_stride : a.k_stride;
-      uint32_t off = loff[i];
-      if (over > 0) off -= (uint32_t)max(lrow[i] - (KB - 1 - over), 0) * (uint32_t)(2 * stride);
-      load_to_lds((is_v ? vbase : kbase) + (int64_t)t * KB * stride, off, buf + part * 1024);
+      const uint16_t* base = (is_v ? vbase : kbase) + (int64_t)t * KB * stride;
+      uint32_t off = loff[kEven ? i / kHalfLoads : i];
+      const int rows = kEven ? i % kHalfLoads * (S::kWaves * kRowsOfLoad) : 0;   // after loff's
+      if (whole_tile) {
+        base += rows * stride;
+      } else {
+        const int r = image_byte(i) / S::kRowBytes;
+        off += (uint32_t)(rows - max(r - last, 0)) * (uint32_t)(2 * stride);
+      }
+      load_to_lds(base, off, buf + i * (S::kWaves * 1024));
     }
   };
 
@@ -349,11 +430,13 @@ __global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_k
     constexpr bool kTurns = kS && kV && S::kTurns;
     auto is_score = [&](int n) { return kTurns ? n % 2 == 0 : kS && n < kOps; };
     auto op_of = [&](int n) { return kTurns ? n / 2 : n % kOps; };
-    const uint32_t kt = kat + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
-    const uint32_t vt = vat + (uint32_t)((t + S::kBufs - 1) % S::kBufs) * (2 * S::kHalf);
+    uint32_t kt = kat + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
+    uint32_t vt = vat + (uint32_t)((t + S::kBufs - 1) % S::kBufs) * (2 * S::kHalf);
     __builtin_amdgcn_s_setprio(1);
     v8bf f[2][kAt];
     auto read = [&](int n) {
+      // the addresses are formed again for every read: kept, they would spill
+      if constexpr (D == 256) asm volatile("" : "+v"(kt), "+v"(vt));
 #pragma unroll
       for (int i = 0; i < kAt; ++i) {
         const int op = op_of(n + i);
@@ -434,6 +517,7 @@ __global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_k
     // phase's products first need it
 #pragma unroll
     for (int u = 0; u < KB / 16; ++u) asm volatile("" : "+v"(pb[u]));
+    asm volatile("" : "+v"(l));
   };
 
   // Phases.  A wave alternates between matrix products (the scores of tile t
@@ -497,41 +581,94 @@ __global__ __launch_bounds__(S::kThreads, 8 / S::kWaves) void prompt_attention_k
 #pragma unroll
     for (int r = 0; r < 16; ++r) odd = fmaf(o[i][r], 0.0f, odd);
   l += __shfl_xor(l, 32);
-  // a row without a score has the sum 0, one whose scores are all NaN the sum
-  // NaN and the maximum -inf
-  const float f = m == kNegInf ? l : 1.0f / l;
-  if (row < nq) {
-    uint16_t* dst = a.out + (int64_t)(q0 + row) * a.out_stride + (int64_t)h * D + 4 * g;
+  int end_c = c;
+  asm volatile("" : "+v"(end_c));                      // worked out again: registers of the loop
+  const int row = row0 + end_c;
+  if (row < nr) {
+    const int64_t token = q0 + row / G;
+    const int h = kvh * G + row % G;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
-        uint2 v;
-        v.x = pack_bf16(o[i][r] * f, o[i][r + 1] * f);
-        v.y = pack_bf16(o[i][r + 2] * f, o[i][r + 3] * f);
-        *reinterpret_cast<uint2*>(dst + 32 * i + 2 * r) = v;
+        const float v[4] = {o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
+        store_row(a, alone, token, h, split, 32 * i + 2 * r + 4 * g, v, m, l, i == 0 && r == 0 && g == 0);
       }
-    if (a.lse && g == 0) a.lse[(int64_t)(q0 + row) * a.NHq + h] = (m + __log2f(l)) * kLn2;
   }
-  if (__any(odd != 0.0f) && mine > 0) {
-    mend_rows<D>(a, q0 + row0, min(kRows, nq - row0), h, k0, nk, min(nk, mine * KB),
-                 a.causal ? row0 + 1 + nk - nq : nk, a.causal);
+  if (__any(odd != 0.0f) && mine > 0)
+    mend_rows<D>(a, q0, nq, row0, min(kRows, nr - row0), kvh, k0, nk_all, key0, min(nk_all, key0 + mine * KB),
+                 alone, split);
+}
+
+// Joins the splits of a row, a wave each: the block that computed it is found
+// again to know how many splits had work.
+template <typename S>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a) {
+  constexpr int D = S::D, KB = S::KB, kPer = D / kWave;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (at >= a.Tq * a.NHq) return;
+  const int64_t token = at / a.NHq;
+  const int h = (int)(at - token * a.NHq);
+  int seq = -1, q0 = 0, nq = 0;
+  for (int b0 = 0; b0 < a.B && seq < 0; b0 += kWave) {
+    int lo = 0;
+    const int n = b0 + lane < a.B ? query_span(a, b0 + lane, &lo) : 0;
+    const unsigned long long hit = __ballot(token >= lo && token < lo + n);
+    if (hit) {
+      const int src = __ffsll(hit) - 1;
+      seq = b0 + src;
+      q0 = __shfl(lo, src);
+      nq = __shfl(n, src);
+    }
   }
+  if (seq < 0) return;
+  const int G = a.NHq / a.NKV;
+  int64_t k0;
+  const int nk = key_span(a, seq, &k0);
+  const int row = (int)(token - q0) * G + h % G;
+  const int last_row = min((row / S::kBlockRows + 1) * S::kBlockRows, nq * G) - 1;
+  const int all_tiles = (keys_seen(a, last_row / G, nq, nk) + KB - 1) / KB;
+  const int each = split_tiles(all_tiles, a.splits);
+  if (all_tiles <= each) return;
+  const int parts = (all_tiles + each - 1) / each;   // at most kMaxSplits = 64
+  const float2 v = lane < parts ? a.part_ml[at * a.splits + lane] : make_float2(kNegInf, 0.0f);
+  const float m = wave_max(v.x);
+  const float f = v.x == kNegInf ? v.y : __builtin_amdgcn_exp2f(v.x - m);
+  const float l = wave_sum(f * v.y);
+  float o[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
+  const float* po = a.part_o + at * a.splits * D + lane * kPer;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float fs = __shfl(f, s);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = fmaf(fs, po[(int64_t)s * D + k], o[k]);
+  }
+  store_row(a, true, token, h, 0, lane * kPer, o, m, l, lane == 0);
 }
 
 template <typename S>
 hipError_t prepare_one() {
-  return prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<S>), S::kLds);
+  hipError_t e = prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<S>), S::kLds);
+  if (e == hipSuccess) e = prepare_kernel(reinterpret_cast<const void*>(&prompt_join_kernel<S>), 0);
+  return e;
 }
+
+// Each sequence ends with at most one part tile.
+int64_t prompt_slots(int64_t Tq, int64_t B, int G) { return Tq * G / kBlockRows + B; }
 
 template <typename S>
 void launch_one(const PromptArgs& p, hipStream_t stream) {
-  // Each sequence ends with at most one part tile; one slot more, so that some
-  // slot is left for the rows behind the last sequence.
-  const int64_t slots = p.Tq / S::kBlockRows + p.B + (p.zero_tail ? 1 : 0);
-  const int64_t per_xcd = (slots * p.NHq + 7) / 8;
-  prompt_attention_kernel<S><<<dim3((unsigned)(8 * per_xcd)), dim3(S::kThreads), S::kLds, stream>>>(
-      p, (int)slots, (int)per_xcd);
+  static_assert(S::kBlockRows == kBlockRows, "rows of a workgroup");
+  // one slot more, so that some slot is left for the rows behind the last sequence
+  const int64_t slots = prompt_slots(p.Tq, p.B, p.NHq / p.NKV) + (p.zero_tail ? 1 : 0);
+  const int64_t groups = slots * p.NKV * p.splits;
+  prompt_attention_kernel<S><<<dim3((unsigned)((groups + 7) / 8 * 8)), dim3(S::kThreads), S::kLds, stream>>>(
+      p, (int)slots);
+  if (p.splits > 1)
+    prompt_join_kernel<S><<<dim3((unsigned)((p.Tq * p.NHq + 3) / 4)), dim3(256), 0, stream>>>(p);
 }
 
 typedef Shape<64, 8, 4> S64;
@@ -549,7 +686,25 @@ hipError_t prepare_prompt_kernels() {
   return e;
 }
 
-hipError_t launch_prompt_attention(const PromptArgs& p, hipStream_t stream) {
+// Splits of the keys where the query tiles leave most of the 256 compute
+// units without work: as many as fill them, each with kLeast tiles if a
+// sequence had all the keys.
+int prompt_splits(int64_t Tq, int64_t Tk, int64_t B, int NHq, int NKV, int D) {
+  if (B == 0 || Tq == 0) return 1;
+  const int64_t units = prompt_slots(Tq, B, NHq / NKV) * NKV;
+  const int64_t most = Tk / ((D <= 128 ? 64 : 32) * kLeast);
+  int64_t s = 256 / units;
+  if (s > most) s = most;
+  return (int)(s < 2 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
+}
+
+size_t prompt_workspace(int64_t Tq, int NHq, int D, int splits) {
+  return splits > 1 ? (size_t)Tq * NHq * splits * (D * sizeof(float) + sizeof(float2)) : 0;
+}
+
+hipError_t launch_prompt_attention(PromptArgs p, void* workspace, hipStream_t stream) {
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.Tq * p.NHq * p.splits * p.D);
   switch (p.D) {
     case 64: launch_one<S64>(p, stream); break;
     case 128: launch_one<S128>(p, stream); break;

@@ -113,7 +113,7 @@ def test_attend_workspace(L):
 
 def prompt(L, **kw):
     a = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cq=P, ck=P, B=2, Tq=9, Tk=9, NHq=4, NKV=2, D=128,
-             causal=1, scale=0.1, out=P, os=512, lse=None, tail=0)
+             causal=1, scale=0.1, out=P, os=512, lse=None, tail=0, ws=None, wsb=0)
     a.update(kw)
     return L.moe_prompt_attention(*a.values(), None)
 
@@ -127,10 +127,19 @@ def prompt(L, **kw):
     (dict(ks=(1 << 24) + 8), UNSUP), (dict(vs=1 << 30), UNSUP),
     (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(cq=None), NULL),
     (dict(ck=None), NULL), (dict(out=None), NULL), (dict(q=P + 8), UNSUP), (dict(v=P + 2), UNSUP),
-    (dict(Tq=0), OK), (dict(B=0), OK),
+    (dict(Tq=0), OK), (dict(B=0), OK), (dict(Tk=4096), WS), (dict(Tk=4096, ws=P, wsb=64), WS),
+    (dict(Tk=4096, ws=P + 8, wsb=1 << 40), UNSUP),
 ])
 def test_prompt(L, kw, want):
     assert prompt(L, **kw) == want
+
+
+def test_prompt_workspace(L):
+    need = L.moe_prompt_attention_workspace_bytes
+    assert need(2, 9, 9, 4, 2, 128) == 0                   # few keys: one split
+    assert need(1, 8192, 8192, 32, 4, 128) == 0            # enough query tiles
+    assert need(2, 9, 4096, 4, 2, 128) > 0
+    assert need(2, 9, 4096, 3, 2, 128) == 0 and need(-1, 9, 4096, 4, 2, 128) == 0
 
 
 def test_binding_refuses_host_tensors():

@@ -423,6 +423,45 @@ def test_prompt(D, NHq, NKV, nq, nk, causal):
     check_prompt(out, lse, q, k, v, nq, nk, causal, D ** -0.5)
 
 
+@pytest.mark.parametrize("D,NHq,NKV,nq,nk,causal", [
+    (128, 8, 1, [1], [5000], True), (64, 7, 1, [40, 3], [1500, 2500], True), (256, 10, 2, [1, 30], [700, 33], True),
+    (192, 6, 2, [2, 0, 60], [900, 50, 61], False), (128, 3, 1, [90], [2000], True), (64, 5, 5, [70, 2], [70, 1600], True),
+    (128, 5, 1, [300], [260], True),
+])
+def test_prompt_groups_and_splits(D, NHq, NKV, nq, nk, causal):
+    """Groups whose rows do not divide a tile, and few queries over many keys
+    (the keys are split and joined, some sequences by one split alone)."""
+    say("prompt groups", D, NHq, NKV, nq, nk, causal)
+    g = gen(D + NHq + sum(nk))
+    q = normal(g, sum(nq), NHq, D)
+    k, v = normal(g, sum(nk), NKV, D), normal(g, sum(nk), NKV, D)
+    out, lse = mm.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), i32(cu(nq)), i32(cu(nk)),
+                                   causal=causal, return_lse=True)
+    check_prompt(out, lse, q, k, v, nq, nk, causal, D ** -0.5)
+
+
+def test_prompt_splits_non_finite():
+    """A value that is not finite in the last split's masked part, a NaN key
+    that some rows see, and a query that is NaN throughout."""
+    say("prompt splits non-finite")
+    g = gen(29)
+    D, NHq, NKV, nq, nk = 128, 4, 2, [6], [3000]
+    q, k, v = normal(g, 6, NHq, D), normal(g, 3000, NKV, D), normal(g, 3000, NKV, D)
+    v[2999, 0, 7] = float("nan")            # the last query alone sees it
+    k[2998, 1, 0] = float("nan")            # the last two queries
+    q[1, 0] = float("nan")
+    out, lse = mm.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), i32([0, 6]), i32([0, 3000]), return_lse=True)
+    nan = torch.zeros(6, NHq, D, dtype=torch.bool)
+    nan[5, :2, 7] = nan[4:, 2:] = nan[1, 0] = True
+    assert torch.equal(torch.isnan(out).cpu(), nan)
+    assert torch.isnan(lse[1, 0]) and torch.isnan(lse[4:, 2:]).all() and torch.isfinite(lse[0]).all()
+    rows = [0, 2, 3]
+    clean = lambda x: torch.nan_to_num(x, nan=0.0)  # noqa: E731
+    for r in rows:
+        check_prompt(out[r:r + 1], lse[r:r + 1], q[r:r + 1], clean(k)[:2995 + r], clean(v)[:2995 + r], [1], [2995 + r],
+                     True, D ** -0.5)
+
+
 def test_prompt_long():
     say("prompt long")
     g = gen(21)
