@@ -206,6 +206,8 @@ struct PromptArgs {
   int splits;                  // of the keys; > 1 needs prompt_workspace(...) bytes of scratch
   float* part_o;               // [Tq][NHq][splits][D]
   float2* part_ml;             // [Tq][NHq][splits] (maximum in powers of two, sum)
+  int G;                       // NHq / NKV
+  int xcd_shift;               // log2(8 / NKV) for 1, 2, 4 or 8 kv heads, else -1
 };
 int prompt_splits(int64_t Tq, int64_t Tk, int64_t B, int NHq, int NKV, int D);
 size_t prompt_workspace(int64_t Tq, int NHq, int D, int splits);

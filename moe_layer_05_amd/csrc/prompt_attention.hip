@@ -86,6 +86,8 @@ struct Shape {
   // the registers go (D = 256 would spill)
   static constexpr int kReadAhead = D == 128 || D == 192 ? 4 : 2;
   static constexpr bool kTurns = D <= 192;
+  // value operands read during the softmax
+  static constexpr int kPre = D == 128 ? 8 : (D == 192 ? 2 : 0);
   // D = 64: two workgroups to a compute unit
   static constexpr int kWavesPerSimd = D == 64 ? 4 : 2;
   // The 16-byte pieces of a row are XOR-ed with a function of the row inside
@@ -140,11 +142,11 @@ __device__ __forceinline__ int query_span(const PromptArgs& p, int b, int* q0) {
   *q0 = (int)lo;
   return (int)(hi - lo);
 }
-__device__ __forceinline__ int key_span(const PromptArgs& p, int b, int64_t* k0) {
+__device__ __forceinline__ int key_span(const PromptArgs& p, int b, int* k0) {
   int64_t lo = p.cu_k[b], hi = p.cu_k[b + 1];
   lo = lo < 0 ? 0 : (lo > p.Tk ? p.Tk : lo);
   hi = hi < lo ? lo : (hi > p.Tk ? p.Tk : hi);
-  *k0 = lo;
+  *k0 = (int)lo;
   return (int)(hi - lo);
 }
 // Keys that query i of nq sees.
@@ -160,30 +162,20 @@ __device__ __forceinline__ int split_tiles(int n, int splits) {
   return each < kLeast ? kLeast : each;
 }
 
-// A finished row, or its part in a split: the sums of features d .. d + N - 1.
+// A finished row, or its part in a split, from a wave: lane's features d ..
 template <int N>
 __device__ __forceinline__ void store_row(const PromptArgs& a, bool alone, int64_t token, int h, int split,
                                           int d, const float (&o)[N], float m, float l, bool first) {
   if (alone) {
-    // a row without a score has the sum 0, one whose scores are all NaN the
-    // sum NaN and the maximum -inf
-    const float f = m == kNegInf ? l : 1.0f / l;
+    const float f = m == kNegInf ? l : 1.0f / l;       // as at the kernel's end
     uint16_t* dst = a.out + token * a.out_stride + (int64_t)h * a.D + d;
-    if constexpr (N == 4) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
-    } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) dst[k] = (uint16_t)pack_bf16(o[k] * f, 0.0f);
-    }
+    for (int k = 0; k < N; ++k) dst[k] = (uint16_t)pack_bf16(o[k] * f, 0.0f);
     if (first && a.lse) a.lse[token * a.NHq + h] = (m + __log2f(l)) * kLn2;
   } else {
     const int64_t at = (token * a.NHq + h) * a.splits + split;
-    if constexpr (N == 4) {
-      *reinterpret_cast<float4*>(a.part_o + at * a.D + d) = make_float4(o[0], o[1], o[2], o[3]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) a.part_o[at * a.D + d + k] = o[k];
-    }
+    for (int k = 0; k < N; ++k) a.part_o[at * a.D + d + k] = o[k];
     if (first) a.part_ml[at] = make_float2(m, l);
   }
 }
@@ -200,7 +192,7 @@ __attribute__((noinline)) __device__ void mend_rows(PromptArgs a, int q0, int nq
                                                     int64_t k0, int nk, int key0, int key1, bool alone, int split) {
   constexpr int kPer = D / kWave;
   const int lane = threadIdx.x & (kWave - 1), f0 = lane * kPer;
-  const int G = a.NHq / a.NKV;
+  const int G = a.G;
   const float scale2 = a.scale * kLog2e;
   int bad = -1;                                        // the last key whose value is not finite
   for (int j = max(key0, keys_seen(a, row0 / G, nq, nk)); j < key1; ++j) {
@@ -244,33 +236,36 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   const int lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int g = lane >> 5, c = lane & 31;
-  const int G = a.NHq / a.NKV;
+  const int G = a.G;
 
   // Workgroup b runs on XCD b & 7.  With 1, 2, 4 or 8 kv heads (or a multiple
   // of 8) each XCD keeps to one kv head at a time, so that its keys stay in
   // that L2, and the XCDs of a head take its slots in turn: the slots with the
   // most keys go first, on all XCDs alike.
   int kvh, rest;
-  if (8 % a.NKV == 0) {
+  if (a.xcd_shift >= 0) {                              // 8 >> xcd_shift kv heads
     const int turn = blockIdx.x & 7;
-    kvh = turn % a.NKV;
-    rest = (blockIdx.x >> 3) * (8 / a.NKV) + turn / a.NKV;
+    kvh = turn & (a.NKV - 1);
+    rest = ((blockIdx.x >> 3) << a.xcd_shift) + (turn >> (3 - a.xcd_shift));
   } else if (a.NKV % 8 == 0) {
-    const int j = blockIdx.x >> 3, heads = a.NKV / 8;
+    const int j = blockIdx.x >> 3, heads = a.NKV >> 3;
     rest = j / heads;
     kvh = (j - rest * heads) * 8 + (blockIdx.x & 7);
   } else {
     rest = blockIdx.x / a.NKV;
     kvh = blockIdx.x - rest * a.NKV;
   }
-  const int x = rest / a.splits, split = rest - x * a.splits;
+  const int x = a.splits == 1 ? rest : rest / a.splits, split = rest - x * a.splits;
   if (x >= slots) return;
 
   // the sequence and tile of slot x: a running sum of the sequences' tiles
-  int seq = -1, tile = 0, q0 = 0, nq = 0, total = 0;
+  int seq = -1, tile = 0, q0 = 0, nq = 0, k0 = 0, nk_all = 0, total = 0;
   for (int b0 = 0; b0 < a.B; b0 += kWave) {
-    int lo = 0;
-    const int n = b0 + lane < a.B ? query_span(a, b0 + lane, &lo) : 0;
+    int lo = 0, klo = 0, n = 0, kn = 0;
+    if (b0 + lane < a.B) {
+      n = query_span(a, b0 + lane, &lo);
+      kn = key_span(a, b0 + lane, &klo);
+    }
     const int nt = (n * G + S::kBlockRows - 1) / S::kBlockRows;
     const int incl = wave_inclusive_sum_dpp(nt);
     const unsigned long long hit = __ballot(x >= total + incl - nt && x < total + incl);
@@ -280,6 +275,8 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
       tile = __shfl(total + incl, src) - 1 - x;       // the last tile first
       q0 = __shfl(lo, src);
       nq = __shfl(n, src);
+      k0 = __shfl(klo, src);
+      nk_all = __shfl(kn, src);
       break;
     }
     total += __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -302,8 +299,8 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   tile = __builtin_amdgcn_readfirstlane(tile);
   q0 = __builtin_amdgcn_readfirstlane(q0);
   nq = __builtin_amdgcn_readfirstlane(nq);
-  int64_t k0;
-  const int nk_all = key_span(a, seq, &k0);
+  k0 = __builtin_amdgcn_readfirstlane(k0);
+  nk_all = __builtin_amdgcn_readfirstlane(nk_all);
   const int nr = nq * G;                              // rows: (query, head of the group)
   const int block0 = tile * S::kBlockRows;
   const int row0 = block0 + wave * kRows;
@@ -324,21 +321,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   const int lim = limit(min(row0 + c, nr - 1));       // lanes past the end repeat the last row
   const int wave_max = row0 < nr ? limit(min(row0 + kRows, nr) - 1) : 0;
 
-  v8bf q[D / 16];
-  {
-    const int row = min(row0 + c, nr - 1);
-    const uint16_t* src = a.q + (int64_t)(q0 + row / G) * a.q_stride + (int64_t)(kvh * G + row % G) * D + g * 8;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      q[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 16 * s));
-  }
-  // the queries are in registers before the first load to LDS: waiting for them
-  // later would wait for those loads as well
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
   const float scale2 = a.scale * kLog2e;
-  const uint16_t* kbase = a.k + (k0 + key0) * a.k_stride + (int64_t)kvh * D;
-  const uint16_t* vbase = a.v + (k0 + key0) * a.v_stride + (int64_t)kvh * D;
+  const uint16_t* kbase = a.k + (int64_t)(k0 + key0) * a.k_stride + (int64_t)kvh * D;
+  const uint16_t* vbase = a.v + (int64_t)(k0 + key0) * a.v_stride + (int64_t)kvh * D;
 
   // This wave's loads of a tile: 1 KB pieces wave, wave + kWaves, .. of K's
   // and then V's LDS image; the lane brings the 16 bytes that belong there.
@@ -383,6 +368,22 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     }
   };
 
+#pragma unroll
+  for (int t = 0; t < S::kAhead; ++t)
+    if (t < tiles) fetch(t);
+  // The queries, behind the first tiles; they are in registers before the loop:
+  // waiting for them in it would wait for the loads to LDS as well.
+  v8bf q[D / 16];
+  {
+    const int row = min(row0 + c, nr - 1);
+    const uint16_t* src = a.q + (int64_t)(q0 + row / G) * a.q_stride + (int64_t)(kvh * G + row % G) * D + g * 8;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      q[s] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(src + 16 * s));
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
+  }
+
   // LDS bytes of the operands: K row c (+ 32 i), piece 2 st + g; V row 16 u +
   // 4 g + (lane & 15) / 4 (+ 8), piece 4 d + x.  The pieces' XOR with the row
   // leaves constants in st and d, since rows differ by multiples of 32 or 16,
@@ -419,17 +420,35 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     return __builtin_bit_cast(v8bf, make_uint4(v0.x, v0.y, v1.x, v1.y));
   };
   // S^T of tile t, and O^T += V^T P^T of tile t - 1 with P as the last softmax
-  // left it, each on request; together they take turns (kTurns), so that an
-  // instruction seldom waits for the one before it.  Operands are read
-  // kReadAhead at a time, one such group ahead of its use.  The wave goes
-  // before the other one of its SIMD meanwhile, whose softmax fills the gaps
-  // (8192 tokens, 32 heads of 128: 543 us, without the priority 561 us).
+  // left it, each on request.  Together: where two score accumulators take
+  // turns (KB = 64), a quarter of the values, then two scores and a value at a
+  // time, then the last values; with one, values and scores in turn (kTurns).
+  // So no instruction waits for the one before it, the first ones find their
+  // operands in registers (ahead, read during the softmax, when the LDS has
+  // less to do) and the scores are ready when the phase ends.  Operands are
+  // read kReadAhead at a time, one such group ahead of its use.  The wave goes
+  // before the other one of its SIMD meanwhile, whose softmax fills the gaps.
+  v8bf ahead[S::kPre ? S::kPre : 1];                   // of the first values
+  auto read_ahead = [&](int t) {
+    const uint32_t vt = vat + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
+#pragma unroll
+    for (int i = 0; i < S::kPre; ++i) ahead[i] = value_operand(vt, i);
+  };
   auto multiply = [&](int t, auto scores, auto values) {
     constexpr bool kS = decltype(scores)::value, kV = decltype(values)::value;
     constexpr int kAll = (kS ? kOps : 0) + (kV ? kOps : 0), kAt = S::kReadAhead;
-    constexpr bool kTurns = kS && kV && S::kTurns;
-    auto is_score = [&](int n) { return kTurns ? n % 2 == 0 : kS && n < kOps; };
-    auto op_of = [&](int n) { return kTurns ? n / 2 : n % kOps; };
+    // instruction n: 2 * op for scores, 2 * op + 1 for values
+    auto at = [&](int n) {
+      if (!kV) return 2 * n;
+      if (!kS) return 2 * n + 1;
+      if (!S::kTurns) return n < kOps ? 2 * n : 2 * (n - kOps) + 1;
+      if (KB == 32) return n % 2 ? n - 1 : n + 1;
+      constexpr int kQ = kOps / 4;
+      if (n < kQ) return 2 * n + 1;
+      if (n >= kAll - kQ) return 2 * (n - kOps) + 1;
+      const int m = n - kQ;
+      return m % 3 == 2 ? 2 * (kQ + m / 3) + 1 : 2 * (m / 3 * 2 + m % 3);
+    };
     uint32_t kt = kat + (uint32_t)(t % S::kBufs) * (2 * S::kHalf);
     uint32_t vt = vat + (uint32_t)((t + S::kBufs - 1) % S::kBufs) * (2 * S::kHalf);
     __builtin_amdgcn_s_setprio(1);
@@ -439,8 +458,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
       if constexpr (D == 256) asm volatile("" : "+v"(kt), "+v"(vt));
 #pragma unroll
       for (int i = 0; i < kAt; ++i) {
-        const int op = op_of(n + i);
-        f[(n / kAt) & 1][i] = is_score(n + i) ? key_operand(kt, op) : value_operand(vt, op);
+        const int op = at(n + i);
+        if (op % 2 == 0) f[(n / kAt) & 1][i] = key_operand(kt, op / 2);
+        else if (op / 2 >= S::kPre) f[(n / kAt) & 1][i] = value_operand(vt, op / 2);
       }
       __builtin_amdgcn_sched_barrier(0);               // reads stay ahead of the products before them
     };
@@ -456,14 +476,14 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
       if (n + kAt < kAll) read(n + kAt);
 #pragma unroll
       for (int i = 0; i < kAt; ++i) {
-        const int op = op_of(n + i);
-        const v8bf x = f[(n / kAt) & 1][i];
-        if (is_score(n + i)) {
+        const int op = at(n + i) / 2;
+        if (at(n + i) % 2 == 0) {
           const int j = op % (KB / 32);
-          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[op / (KB / 32)], s[j], 0, 0, 0);
+          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[(n / kAt) & 1][i], q[op / (KB / 32)], s[j], 0, 0, 0);
         } else {
           const int d = op % (D / 32);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, pb[op / (D / 32)], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op < S::kPre ? ahead[op < S::kPre ? op : 0] : f[(n / kAt) & 1][i],
+                                                         pb[op / (D / 32)], o[d], 0, 0, 0);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -541,9 +561,6 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-#pragma unroll
-  for (int t = 0; t < S::kAhead; ++t)
-    if (t < tiles) fetch(t);
   auto before_softmax = [&](int t) {
     if (late) even(t + 1);
     else barrier();
@@ -559,11 +576,13 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
 #pragma clang loop unroll(disable)
     for (int t = 0; t < mine - 1; ++t) {
       before_softmax(t);
+      read_ahead(t);
       softmax(t);
       after_softmax(t);
       multiply(t + 1, std::true_type{}, std::true_type{});
     }
     before_softmax(mine - 1);
+    read_ahead(mine - 1);
     softmax(mine - 1);
     after_softmax(mine - 1);
     multiply(mine, std::false_type{}, std::true_type{});
@@ -584,16 +603,40 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   int end_c = c;
   asm volatile("" : "+v"(end_c));                      // worked out again: registers of the loop
   const int row = row0 + end_c;
-  if (row < nr) {
-    const int64_t token = q0 + row / G;
-    const int h = kvh * G + row % G;
+  const int64_t token = q0 + min(row, nr - 1) / G;
+  const int h = kvh * G + min(row, nr - 1) % G;
+  if (alone) {
+    // a row without a score has the sum 0, one whose scores are all NaN the
+    // sum NaN and the maximum -inf
+    const float f = m == kNegInf ? l : 1.0f / l;
+    uint16_t* dst = a.out + token * a.out_stride + (int64_t)h * D + 8 * g;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const float v[4] = {o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]};
-        store_row(a, alone, token, h, split, 32 * i + 2 * r + 4 * g, v, m, l, i == 0 && r == 0 && g == 0);
+      for (int r = 0; r < 16; r += 8) {
+        // registers r .. r + 3 of both halves are 8 features, r + 4 .. the next
+        // 8: the halves exchange, so that each stores 16 bytes
+        uint32_t x[2], y[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[j] = pack_bf16(o[i][r + 2 * j] * f, o[i][r + 2 * j + 1] * f);
+          y[j] = pack_bf16(o[i][r + 4 + 2 * j] * f, o[i][r + 5 + 2 * j] * f);
+          const auto swapped = __builtin_amdgcn_permlane32_swap(x[j], y[j], false, false);
+          x[j] = swapped[0];
+          y[j] = swapped[1];
+        }
+        if (row < nr) *reinterpret_cast<uint4*>(dst + 32 * i + 2 * r) = make_uint4(x[0], x[1], y[0], y[1]);
       }
+    if (row < nr && a.lse && g == 0) a.lse[token * a.NHq + h] = (m + __log2f(l)) * kLn2;
+  } else if (row < nr) {
+    const int64_t at = (token * a.NHq + h) * a.splits + split;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        *reinterpret_cast<float4*>(a.part_o + at * D + 32 * i + 2 * r + 4 * g) =
+            make_float4(o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]);
+    if (g == 0) a.part_ml[at] = make_float2(m, l);
   }
   if (__any(odd != 0.0f) && mine > 0)
     mend_rows<D>(a, q0, nq, row0, min(kRows, nr - row0), kvh, k0, nk_all, key0, min(nk_all, key0 + mine * KB),
@@ -623,8 +666,8 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a) {
     }
   }
   if (seq < 0) return;
-  const int G = a.NHq / a.NKV;
-  int64_t k0;
+  const int G = a.G;
+  int k0;
   const int nk = key_span(a, seq, &k0);
   const int row = (int)(token - q0) * G + h % G;
   const int last_row = min((row / S::kBlockRows + 1) * S::kBlockRows, nq * G) - 1;
@@ -703,6 +746,8 @@ size_t prompt_workspace(int64_t Tq, int NHq, int D, int splits) {
 }
 
 hipError_t launch_prompt_attention(PromptArgs p, void* workspace, hipStream_t stream) {
+  p.G = p.NHq / p.NKV;
+  p.xcd_shift = p.NKV == 1 ? 3 : (p.NKV == 2 ? 2 : (p.NKV == 4 ? 1 : (p.NKV == 8 ? 0 : -1)));
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.Tq * p.NHq * p.splits * p.D);
   switch (p.D) {
