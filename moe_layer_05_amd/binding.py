@@ -6,6 +6,7 @@ fallback: if the library is missing or fails to load, every call raises.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -350,34 +351,34 @@ def _vector(t, dtype, n, name, dev):
     return t.data_ptr()
 
 
-class _OnStream:
-    """Makes a call's device and stream torch's current ones for the time of
-    the call: outputs and scratch made inside belong to that stream, and
-    inputs of another stream are kept from reuse until the call's work is
-    done.  The usual call, on the current stream of the current device, needs
-    none of this (scope None)."""
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, dev, stream, inputs):
-        self.scope = None
-        if stream is None and torch._C._cuda_getDevice() == dev:
-            self.raw = torch._C._cuda_getCurrentRawStream(dev)
-            return
-        current = torch.cuda.current_stream(dev)
-        if stream is None:
-            stream = current
-        elif stream.device.index != dev:
-            raise ValueError(f"stream must be on device {dev}, got one on {stream.device}")
-        self.raw = stream.cuda_stream
-        if stream != current:
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-        self.scope = torch.cuda.stream(stream)
-        self.scope.__enter__()
 
-    def done(self):
-        if self.scope is not None:
-            self.scope.__exit__(None, None, None)
+def _elsewhere(dev, stream, inputs):
+    """The scope of a call that is not on the current stream of the current
+    device: that device and ``stream`` become torch's current ones, so that
+    outputs and scratch made inside belong to them, and inputs of another
+    stream are kept from reuse until the call's work is done."""
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream.device.index != dev:
+        raise ValueError(f"stream must be on device {dev}, got one on {stream.device}")
+    if stream != current:
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _here(dev, stream):
+    return stream is None and _device() == dev
+
+
+@functools.lru_cache(maxsize=1024)
+def _prompt_workspace(*shape):
+    return lib().moe_prompt_attention_workspace_bytes(*shape)
 
 
 def _no_overlap(out, inputs, name):
@@ -439,20 +440,19 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
     qos = NHq * D if q_out is None else _inner_out(q_out, q, (T, NHq, D), "q_out", dev)
     if k is not None:
         kos = NHk * D if k_out is None else _inner_out(k_out, k, (T, NHk, D), "k_out", dev)
-    on = _OnStream(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out))
-    try:
-        if q_out is None:
-            q_out = torch.empty_like(q)              # contiguous, whatever q's token stride
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty_like(k)
-            kop = k_out.data_ptr()
-        _check(lib().moe_qk_norm_rope(
-            q.data_ptr(), qs, kp, ks, pp, cos_sin.data_ptr(), cos_sin.shape[0], T, NHq, NHk, D, R,
-            1 if interleaved else 0, qw, kw, f32, eps, q_out.data_ptr(), qos, kop, kos, on.raw),
-            "moe_qk_norm_rope")
-    finally:
-        on.done()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out)):
+            return qk_norm_rope(q, k, positions, cos_sin, R, q_weight, k_weight, eps, interleaved, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q)              # contiguous, whatever q's token stride
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        kop = k_out.data_ptr()
+    _check(lib().moe_qk_norm_rope(
+        q.data_ptr(), qs, kp, ks, pp, cos_sin.data_ptr(), cos_sin.shape[0], T, NHq, NHk, D, R,
+        1 if interleaved else 0, qw, kw, f32, eps, q_out.data_ptr(), qos, kop, kos, _raw_stream(dev)),
+        "moe_qk_norm_rope")
     return q_out, k_out
 
 
@@ -532,12 +532,11 @@ class KVCache4:
             raise ValueError(f"k must be [T, {self.NKV}, {self.D}]")
         vs = _heads(v, "v", self._dev, (T, NKV, D))[3]
         at = self._places(block_table, start, cu_seqlens, T)
-        on = _OnStream(self._dev, stream, (self.pages, k, v, block_table, start, cu_seqlens))
-        try:
-            _check(lib().moe_cache4_write(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at, on.raw),
-                   "moe_cache4_write")
-        finally:
-            on.done()
+        if not _here(self._dev, stream):
+            with _elsewhere(self._dev, stream, (self.pages, k, v, block_table, start, cu_seqlens)):
+                return self.write(k, v, block_table, start, cu_seqlens)
+        _check(lib().moe_cache4_write(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at, _raw_stream(self._dev)),
+               "moe_cache4_write")
 
     def read(self, block_table, start, cu_seqlens, T, k=None, v=None, stream=None):
         """(k, v) bfloat16 [T, NKV, D]: the values that the cache holds of
@@ -555,15 +554,14 @@ class KVCache4:
             ks, vs = _heads(k, "k", self._dev, shape)[3], _heads(v, "v", self._dev, shape)[3]
             _no_overlap(k, (self.pages, v), "k")
             _no_overlap(v, (self.pages,), "v")
-        on = _OnStream(self._dev, stream, (self.pages, block_table, start, cu_seqlens, k, v))
-        try:
-            if fresh:
-                k = self.pages.new_empty(shape, dtype=torch.bfloat16)
-                v = torch.empty_like(k)
-            _check(lib().moe_cache4_read(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at,
-                                         1 if fresh else 0, on.raw), "moe_cache4_read")
-        finally:
-            on.done()
+        if not _here(self._dev, stream):
+            with _elsewhere(self._dev, stream, (self.pages, block_table, start, cu_seqlens, k, v)):
+                return self.read(block_table, start, cu_seqlens, T, k, v)
+        if fresh:
+            k = self.pages.new_empty(shape, dtype=torch.bfloat16)
+            v = torch.empty_like(k)
+        _check(lib().moe_cache4_read(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at, 1 if fresh else 0,
+                                     _raw_stream(self._dev)), "moe_cache4_read")
         return k, v
 
     def attend(self, q, block_table, lens, scale=None, out=None, return_lse=False, stream=None):
@@ -583,21 +581,20 @@ class KVCache4:
         if out is not None:
             os_ = _heads(out, "out", dev, (B, NHq, D))[3]
             _no_overlap(out, (q, self.pages), "out")
+        if not _here(dev, stream):
+            with _elsewhere(dev, stream, (self.pages, q, block_table, lens, out)):
+                return self.attend(q, block_table, lens, scale, out, return_lse)
         L = lib()
+        # scratch of this call alone: graphs that hold it may run side by side
         nbytes = L.moe_cache4_attend_workspace_bytes(self._c, B, NHq, n)
-        on = _OnStream(dev, stream, (self.pages, q, block_table, lens, out))
-        try:
-            if out is None:
-                out = torch.empty_like(q)
-            lse = q.new_empty((B, NHq), dtype=torch.float32) if return_lse else None
-            # scratch of this call alone: graphs that hold it may run side by side
-            ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
-            _check(L.moe_cache4_attend(
-                self._c, q.data_ptr(), qs, tp, ts, n, lp, B, NHq, D ** -0.5 if scale is None else scale,
-                out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
-                None if ws is None else ws.data_ptr(), nbytes, on.raw), "moe_cache4_attend")
-        finally:
-            on.done()
+        ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
+        if out is None:
+            out = torch.empty_like(q)
+        lse = q.new_empty((B, NHq), dtype=torch.float32) if return_lse else None
+        _check(L.moe_cache4_attend(
+            self._c, q.data_ptr(), qs, tp, ts, n, lp, B, NHq, D ** -0.5 if scale is None else scale,
+            out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
+            None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)), "moe_cache4_attend")
         return (out, lse) if return_lse else out
 
 
@@ -631,22 +628,20 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     if not fresh:
         os_ = _heads(out, "out", dev, (Tq, NHq, D))[3]
         _no_overlap(out, (q, k, v), "out")
-    L = lib()
-    nbytes = L.moe_prompt_attention_workspace_bytes(B, Tq, Tk, NHq, NKV, D)
-    on = _OnStream(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out))
-    try:
-        if fresh:
-            out = torch.empty_like(q)
-        lse = q.new_empty((Tq, NHq), dtype=torch.float32) if return_lse else None
-        # scratch of this call alone: graphs that hold it may run side by side
-        ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
-        _check(L.moe_prompt_attention(
-            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, B, Tq, Tk, NHq, NKV, D,
-            1 if causal else 0, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-            None if lse is None else lse.data_ptr(), 3 if fresh else 2,
-            None if ws is None else ws.data_ptr(), nbytes, on.raw), "moe_prompt_attention")
-    finally:
-        on.done()
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out)):
+            return prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, out, return_lse)
+    # scratch of this call alone: graphs that hold it may run side by side
+    nbytes = _prompt_workspace(B, Tq, Tk, NHq, NKV, D)
+    ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
+    if fresh:
+        out = torch.empty_like(q)
+    lse = q.new_empty((Tq, NHq), dtype=torch.float32) if return_lse else None
+    _check(lib().moe_prompt_attention(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, B, Tq, Tk, NHq, NKV, D,
+        1 if causal else 0, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+        None if lse is None else lse.data_ptr(), 3 if fresh else 2,
+        None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)), "moe_prompt_attention")
     return (out, lse) if return_lse else out
 
 
