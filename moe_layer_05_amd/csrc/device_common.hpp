@@ -46,6 +46,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, v2bf));
 }
 
+// Sixteen bytes of a stream that is not read again soon, past the caches.
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p)));
+}
+__device__ __forceinline__ void store_stream(uint4* p, const uint4& v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(v4u, v), reinterpret_cast<v4u*>(p));
+}
+
 // Four consecutive partial outputs at element `idx` of a partial-row buffer:
 // float32, or bfloat16 (nearest even) when `bf16`.
 __device__ __forceinline__ void store_part4(void* buf, bool bf16, int64_t idx, float a, float b,

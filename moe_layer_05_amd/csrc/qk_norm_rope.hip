@@ -19,6 +19,13 @@
 // f < R/2 is R/16 lanes further on, fetched by one shuffle of four words.
 // Every head is read whole before it is written, so a head may be written
 // onto itself.
+//
+// HBM-bound (latency-bound below some hundred tokens): every head read and
+// written once, the table's rows of the call's positions read once.  Measured:
+// 4096 tokens, 72 heads of 128: 31 us = 4.9 TB/s; 1023 tokens, 32 heads of 192,
+// 64 features rotated, no norm: 5.9 us = 4.3 TB/s; 16 tokens, 18 heads: 3.2 us.
+// Outputs go past the L2 (through it 34 and 6.6 us); inputs do not (7.1 us for
+// the second).
 #include "device_common.hpp"
 #include "internal.hpp"
 
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(NormRopeArgs a) 
       o.y = pack_bf16(v[2], v[3]);
       o.z = pack_bf16(v[4], v[5]);
       o.w = pack_bf16(v[6], v[7]);
-      y[(int64_t)h * d8 + j] = o;
+      store_stream(y + ((int64_t)h * d8 + j), o);
     }
   }
 }
