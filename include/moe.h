@@ -394,23 +394,37 @@ moe_status moe_fused_forward_noalloc(const moe_fused_args* args, hipStream_t str
  * over the pairs (i, i + R/2) (interleaved == 0) or (2i, 2i + 1), features
  * R..D-1 passing through as z; float32 throughout, rounded once.
  *
- *   q, k       [T][NHq][D], [T][NHk][D] bfloat16, 16-byte aligned; NHk may be
- *              0 (k, k_weight, k_out unused)
+ *   q, k       [T][NHq][D], [T][NHk][D] bfloat16, 16-byte aligned; NHk may
+ *              be 0 (k, k_weight, k_out unused)
  *   positions, cos_sin   as in moe_inv_rope_fp8_quant_per_head
  *   q_weight, k_weight   [D] bfloat16, or float32 with weights_f32; NULL: no
  *              norm of that side; 16-byte aligned
  *   q_out, k_out   as q, k (out); may be q, k themselves, and must not
  *              overlap them otherwise
  * Supported: D % 8 == 0 and D <= 512; R even, 0 < R <= D, R % 16 == 0
- * (R % 8 == 0 when interleaved); eps >= 0 and finite.
+ * (R % 8 == 0 when interleaved); eps >= 0 and finite; T * (NHq + NHk) < 2^32.
  */
-moe_status moe_qk_norm_rope(const void* q, int64_t q_token_stride, const void* k,
-                            int64_t k_token_stride, const int64_t* positions,
-                            const float* cos_sin, int64_t max_pos, int64_t T, int32_t NHq,
-                            int32_t NHk, int32_t D, int32_t R, int32_t interleaved,
-                            const void* q_weight, const void* k_weight, int32_t weights_f32,
-                            float eps, void* q_out, int64_t q_out_token_stride, void* k_out,
-                            int64_t k_out_token_stride, hipStream_t stream);
+typedef struct {
+  const void* q;
+  int64_t q_token_stride;
+  const void* k;
+  int64_t k_token_stride;
+  const int64_t* positions;
+  const float* cos_sin;
+  int64_t max_pos;
+  int64_t T;
+  const void* q_weight;
+  const void* k_weight;
+  void* q_out;
+  int64_t q_out_token_stride;
+  void* k_out;
+  int64_t k_out_token_stride;
+  int32_t NHq, NHk, D, R;
+  int32_t interleaved;
+  int32_t weights_f32;
+  float eps;
+} moe_qk_norm_rope_args;
+moe_status moe_qk_norm_rope(const moe_qk_norm_rope_args* args, hipStream_t stream);
 
 /*
  * A paged cache of keys and values in 4 bits.  A group of 32 consecutive
@@ -444,32 +458,47 @@ typedef struct {
 size_t moe_cache4_page_bytes(int32_t page_size, int32_t NKV, int32_t D);
 
 /*
- * Quantises the keys and values of packed tokens into the cache.  Token
- * cu_seqlens[b] + i goes to position start[b] + i of sequence b; position p
- * lies in page block_table[b][p / page_size].
- *   k, v         [T][NKV][D] bfloat16, 16-byte aligned
+ * Packed tokens and their places in the cache.  Token cu_seqlens[b] + i is at
+ * position start[b] + i of sequence b; position p lies in page
+ * block_table[b][p / page_size].
+ *   k, v         [T][NKV][D] bfloat16, 16-byte aligned; read by
+ *                moe_cache4_write, written by moe_cache4_read
  *   block_table  [B][max_pages] int32, rows table_stride apart
  *   start        [B] int32
  *   cu_seqlens   [B + 1] int32, or NULL: one token per sequence (T == B)
- * A token is skipped if its position is negative or behind max_pages pages, or
- * if its page id is not in [0, num_pages): padded sequences of a captured
- * batch take a start of -1.  Positions of two sequences that share a page must
- * differ (as must any two tokens' places), or the place holds a mixture.
+ *   zero_tail    moe_cache4_read: != 0 zeroes the rows of k and v behind the
+ *                last sequence
  */
-moe_status moe_cache4_write(const moe_cache4* cache, const void* k, int64_t k_token_stride,
-                            const void* v, int64_t v_token_stride, const int32_t* block_table,
-                            int64_t table_stride, int32_t max_pages, const int32_t* start,
-                            const int32_t* cu_seqlens, int32_t B, int64_t T, hipStream_t stream);
+typedef struct {
+  void* k;
+  int64_t k_token_stride;
+  void* v;
+  int64_t v_token_stride;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* start;
+  const int32_t* cu_seqlens;
+  int64_t T;
+  int32_t B;
+  int32_t max_pages;
+  int32_t zero_tail;
+} moe_cache4_tokens;
 
 /*
- * Reads such tokens back as bfloat16 k, v [T][NKV][D] (out); places that
- * moe_cache4_write would skip read as zeros.  zero_tail != 0 also zeroes the
- * rows behind the last sequence.
+ * Quantises the tokens' keys and values into the cache.  A token is skipped if
+ * its position is negative or behind max_pages pages, or if its page id is not
+ * in [0, num_pages): padded sequences of a captured batch take a start of -1.
+ * Positions of two sequences that share a page must differ (as must any two
+ * tokens' places), or the place holds a mixture.
  */
-moe_status moe_cache4_read(const moe_cache4* cache, void* k, int64_t k_token_stride, void* v,
-                           int64_t v_token_stride, const int32_t* block_table,
-                           int64_t table_stride, int32_t max_pages, const int32_t* start,
-                           const int32_t* cu_seqlens, int32_t B, int64_t T, int32_t zero_tail,
+moe_status moe_cache4_write(const moe_cache4* cache, const moe_cache4_tokens* tokens,
+                            hipStream_t stream);
+
+/*
+ * Reads the tokens' keys and values back; places that moe_cache4_write would
+ * skip read as zeros.
+ */
+moe_status moe_cache4_read(const moe_cache4* cache, const moe_cache4_tokens* tokens,
                            hipStream_t stream);
 
 /*
@@ -490,13 +519,26 @@ moe_status moe_cache4_read(const moe_cache4* cache, void* k, int64_t k_token_str
  * Supported: NHq a multiple of NKV; B <= 65535; scale positive and finite;
  * max_pages * page_size <= 2^28.
  */
+typedef struct {
+  const void* q;
+  int64_t q_token_stride;
+  const int32_t* block_table;
+  int64_t table_stride;
+  const int32_t* lens;
+  void* out;
+  int64_t out_token_stride;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t B;
+  int32_t max_pages;
+  int32_t NHq;
+  float scale;
+} moe_cache4_attend_args;
 size_t moe_cache4_attend_workspace_bytes(const moe_cache4* cache, int32_t B, int32_t NHq,
                                          int32_t max_pages);
-moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_token_stride,
-                             const int32_t* block_table, int64_t table_stride, int32_t max_pages,
-                             const int32_t* lens, int32_t B, int32_t NHq, float scale, void* out,
-                             int64_t out_token_stride, float* lse, void* workspace,
-                             size_t workspace_bytes, hipStream_t stream);
+moe_status moe_cache4_attend(const moe_cache4* cache, const moe_cache4_attend_args* args,
+                             hipStream_t stream);
 
 /*
  * Attention of packed prompts.  Query i of a sequence of nq queries and nk
@@ -518,15 +560,29 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_t
  * finite; k and v token strides <= 2^24; Tq * NHq and Tk < 2^31 - 2^16;
  * (B + 8) * NKV < 2^29.
  */
+typedef struct {
+  const void* q;
+  int64_t q_token_stride;
+  const void* k;
+  int64_t k_token_stride;
+  const void* v;
+  int64_t v_token_stride;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  void* out;
+  int64_t out_token_stride;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t Tq, Tk;
+  int32_t B, NHq, NKV, D;
+  int32_t causal;
+  int32_t zero_tail;
+  float scale;
+} moe_prompt_attention_args;
 size_t moe_prompt_attention_workspace_bytes(int32_t B, int64_t Tq, int64_t Tk, int32_t NHq,
                                             int32_t NKV, int32_t D);
-moe_status moe_prompt_attention(const void* q, int64_t q_token_stride, const void* k,
-                                int64_t k_token_stride, const void* v, int64_t v_token_stride,
-                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
-                                int32_t B, int64_t Tq, int64_t Tk, int32_t NHq, int32_t NKV,
-                                int32_t D, int32_t causal, float scale, void* out,
-                                int64_t out_token_stride, float* lse, int32_t zero_tail,
-                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+moe_status moe_prompt_attention(const moe_prompt_attention_args* args, hipStream_t stream);
 
 #ifdef __cplusplus
 }

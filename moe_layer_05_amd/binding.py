@@ -8,6 +8,7 @@ fallback: if the library is missing or fails to load, every call raises.
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -65,6 +66,16 @@ class Cache4(ctypes.Structure):
         ("NKV", ctypes.c_int32),
         ("D", ctypes.c_int32),
     ]
+
+
+# Argument structures of the attention side, as bytes: packing all fields of a
+# call at once takes a third of the time of converting them one by one.
+# (moe_qk_norm_rope_args, moe_cache4_tokens, moe_cache4_attend_args and
+# moe_prompt_attention_args; fields in the order of include/moe.h)
+pack_norm_rope = struct.Struct("=QqQqQQqqQQQqQq6if4x").pack
+pack_tokens = struct.Struct("=QqQqQqQQq3i4x").pack
+pack_attend = struct.Struct("=QqQqQQqQQQ3if").pack
+pack_prompt = struct.Struct("=QqQqQqQQQqQQQqq6if4x").pack
 
 
 NO_SECTION = ctypes.c_size_t(-1).value
@@ -134,34 +145,14 @@ _SIGS = {
         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
         ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
-    "moe_qk_norm_rope": (ctypes.c_int, [
-        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
-        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
-        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
-        ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
-        ctypes.c_int64, ctypes.c_void_p]),
+    "moe_qk_norm_rope": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
     "moe_cache4_page_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
-    "moe_cache4_write": (ctypes.c_int, [
-        ctypes.POINTER(Cache4), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
-        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
-        ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
-    "moe_cache4_read": (ctypes.c_int, [
-        ctypes.POINTER(Cache4), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
-        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
-        ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
+    "moe_cache4_write": (ctypes.c_int, [ctypes.POINTER(Cache4), ctypes.c_char_p, ctypes.c_void_p]),
+    "moe_cache4_read": (ctypes.c_int, [ctypes.POINTER(Cache4), ctypes.c_char_p, ctypes.c_void_p]),
     "moe_cache4_attend_workspace_bytes": (ctypes.c_size_t, [
         ctypes.POINTER(Cache4), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
-    "moe_cache4_attend": (ctypes.c_int, [
-        ctypes.POINTER(Cache4), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
-        ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
-        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
-        ctypes.c_void_p]),
-    "moe_prompt_attention": (ctypes.c_int, [
-        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
-        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
-        ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
-        ctypes.c_float, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
-        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_cache4_attend": (ctypes.c_int, [ctypes.POINTER(Cache4), ctypes.c_char_p, ctypes.c_void_p]),
+    "moe_prompt_attention": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p]),
     "moe_prompt_attention_workspace_bytes": (ctypes.c_size_t, [
         ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
         ctypes.c_int32]),
@@ -376,30 +367,35 @@ def _here(dev, stream):
     return stream is None and _device() == dev
 
 
+# The sizes of scratch go by shapes alone.
+@functools.lru_cache(maxsize=1024)
+def _attend_workspace(page_size, NKV, D, B, NHq, max_pages):
+    one = Cache4(None, 1, page_size, NKV, D)
+    return lib().moe_cache4_attend_workspace_bytes(ctypes.byref(one), B, NHq, max_pages)
+
+
 @functools.lru_cache(maxsize=1024)
 def _prompt_workspace(*shape):
     return lib().moe_prompt_attention_workspace_bytes(*shape)
 
 
-def _no_overlap(out, inputs, name):
-    """Refuses an output whose memory meets an input's."""
-    def span(t):
-        if t.numel() == 0:
-            return 0, 0
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    a0, a1 = span(out)
-    for t in inputs:
-        b0, b1 = span(t)
-        if a0 < b1 and b0 < a1:
-            raise ValueError(f"{name} must not overlap an input")
+def _span(t, T, H, D, stride):
+    """The bytes [from, to) that heads [T, H, D] reach."""
+    p = t.data_ptr()
+    return p, p + 2 * ((T - 1) * stride + H * D) if T else p
 
 
-def _inner_out(y, x, shape, name, dev):
+def _apart(name, a, b):
+    """Refuses an output whose span meets an input's."""
+    if a[0] < b[1] and b[0] < a[1]:
+        raise ValueError(f"{name} must not overlap an input")
+
+
+def _inner_out(y, x, T, H, D, stride, name, dev):
     """The token stride of an output that may be its input itself."""
-    ys = _heads(y, name, dev, shape)[3]
-    if y.data_ptr() != x.data_ptr() or y.stride() != x.stride():
-        _no_overlap(y, (x,), name)
+    ys = _heads(y, name, dev, (T, H, D))[3]
+    if y.data_ptr() != x.data_ptr() or ys != stride:
+        _apart(name, _span(y, T, H, D, ys), _span(x, T, H, D, stride))
     return ys
 
 
@@ -414,8 +410,7 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
     inputs otherwise."""
     T, NHq, D, qs = _heads(q, "q")
     dev = q.get_device()
-    NHk = ks = kos = 0
-    kp = kop = None
+    NHk = ks = kos = kp = kop = f32 = qw = kw = 0
     if k is not None:
         Tk, NHk, Dk, ks = _heads(k, "k", dev)
         if Tk != T or Dk != D:
@@ -429,7 +424,6 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
     if cos_sin.dim() != 2 or cos_sin.shape[1] != R or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
         raise ValueError(f"cos_sin must be [max_pos, {R}], contiguous, on device {dev}")
     w = q_weight if q_weight is not None else k_weight
-    f32, qw, kw = 0, None, None
     if w is not None:
         f32 = int(w.dtype is torch.float32)
         wt = torch.float32 if f32 else torch.bfloat16
@@ -437,9 +431,9 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
             qw = _vector(q_weight, wt, D, "q_weight", dev)
         if k_weight is not None:
             kw = _vector(k_weight, wt, D, "k_weight", dev)
-    qos = NHq * D if q_out is None else _inner_out(q_out, q, (T, NHq, D), "q_out", dev)
+    qos = NHq * D if q_out is None else _inner_out(q_out, q, T, NHq, D, qs, "q_out", dev)
     if k is not None:
-        kos = NHk * D if k_out is None else _inner_out(k_out, k, (T, NHk, D), "k_out", dev)
+        kos = NHk * D if k_out is None else _inner_out(k_out, k, T, NHk, D, ks, "k_out", dev)
     if not _here(dev, stream):
         with _elsewhere(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out)):
             return qk_norm_rope(q, k, positions, cos_sin, R, q_weight, k_weight, eps, interleaved, q_out, k_out)
@@ -449,9 +443,9 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
         if k_out is None:
             k_out = torch.empty_like(k)
         kop = k_out.data_ptr()
-    _check(lib().moe_qk_norm_rope(
-        q.data_ptr(), qs, kp, ks, pp, cos_sin.data_ptr(), cos_sin.shape[0], T, NHq, NHk, D, R,
-        1 if interleaved else 0, qw, kw, f32, eps, q_out.data_ptr(), qos, kop, kos, _raw_stream(dev)),
+    _check(lib().moe_qk_norm_rope(pack_norm_rope(
+        q.data_ptr(), qs, kp, ks, pp, cos_sin.data_ptr(), cos_sin.shape[0], T, qw, kw, q_out.data_ptr(),
+        qos, kop, kos, NHq, NHk, D, R, 1 if interleaved else 0, f32, eps), _raw_stream(dev)),
         "moe_qk_norm_rope")
     return q_out, k_out
 
@@ -492,6 +486,7 @@ class KVCache4:
         self.pages = pages
         self.num_pages, self.NKV, self.page_size, self.D = n, NKV, 16 * tiles, row // 17
         self._dev = pages.get_device()
+        self._span = pages.data_ptr(), pages.data_ptr() + pages.numel()
         self._c = ctypes.byref(Cache4(pages.data_ptr(), n, NKV=NKV, page_size=16 * tiles, D=row // 17))
 
     def _table(self, t, B):
@@ -516,10 +511,11 @@ class KVCache4:
         if cu_seqlens is not None:
             cu = _vector(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev)
         elif T == B:
-            cu = None
+            cu = 0
         else:
             raise ValueError(f"{T} tokens for {B} sequences need cu_seqlens")
-        return (*self._table(block_table, B), sp, cu, B, T)
+        tp, ts, n = self._table(block_table, B)
+        return tp, ts, sp, cu, T, B, n
 
     def write(self, k, v, block_table, start, cu_seqlens=None, stream=None):
         """Quantises bfloat16 keys and values [T, NKV, D] of packed sequences
@@ -535,8 +531,8 @@ class KVCache4:
         if not _here(self._dev, stream):
             with _elsewhere(self._dev, stream, (self.pages, k, v, block_table, start, cu_seqlens)):
                 return self.write(k, v, block_table, start, cu_seqlens)
-        _check(lib().moe_cache4_write(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at, _raw_stream(self._dev)),
-               "moe_cache4_write")
+        _check(lib().moe_cache4_write(self._c, pack_tokens(k.data_ptr(), ks, v.data_ptr(), vs, *at, 0),
+                                      _raw_stream(self._dev)), "moe_cache4_write")
 
     def read(self, block_table, start, cu_seqlens, T, k=None, v=None, stream=None):
         """(k, v) bfloat16 [T, NKV, D]: the values that the cache holds of
@@ -552,15 +548,19 @@ class KVCache4:
         ks = vs = self.NKV * self.D
         if not fresh:
             ks, vs = _heads(k, "k", self._dev, shape)[3], _heads(v, "v", self._dev, shape)[3]
-            _no_overlap(k, (self.pages, v), "k")
-            _no_overlap(v, (self.pages,), "v")
+            kspan, vspan = _span(k, *shape, ks), _span(v, *shape, vs)
+            _apart("k", kspan, self._span)
+            _apart("v", vspan, self._span)
+            if k.data_ptr() == v.data_ptr() or ks == self.NKV * self.D == vs:
+                _apart("k", kspan, vspan)        # (interleaved rows of one tensor are told apart)
         if not _here(self._dev, stream):
             with _elsewhere(self._dev, stream, (self.pages, block_table, start, cu_seqlens, k, v)):
                 return self.read(block_table, start, cu_seqlens, T, k, v)
         if fresh:
             k = self.pages.new_empty(shape, dtype=torch.bfloat16)
             v = torch.empty_like(k)
-        _check(lib().moe_cache4_read(self._c, k.data_ptr(), ks, v.data_ptr(), vs, *at, 1 if fresh else 0,
+        _check(lib().moe_cache4_read(self._c, pack_tokens(k.data_ptr(), ks, v.data_ptr(), vs, *at,
+                                                          1 if fresh else 0),
                                      _raw_stream(self._dev)), "moe_cache4_read")
         return k, v
 
@@ -580,21 +580,22 @@ class KVCache4:
         os_ = NHq * D
         if out is not None:
             os_ = _heads(out, "out", dev, (B, NHq, D))[3]
-            _no_overlap(out, (q, self.pages), "out")
+            ospan = _span(out, B, NHq, D, os_)
+            _apart("out", ospan, _span(q, B, NHq, D, qs))
+            _apart("out", ospan, self._span)
         if not _here(dev, stream):
             with _elsewhere(dev, stream, (self.pages, q, block_table, lens, out)):
                 return self.attend(q, block_table, lens, scale, out, return_lse)
-        L = lib()
         # scratch of this call alone: graphs that hold it may run side by side
-        nbytes = L.moe_cache4_attend_workspace_bytes(self._c, B, NHq, n)
+        nbytes = _attend_workspace(self.page_size, self.NKV, D, B, NHq, n)
         ws = q.new_empty(nbytes // 4, dtype=torch.float32) if nbytes else None
         if out is None:
             out = torch.empty_like(q)
         lse = q.new_empty((B, NHq), dtype=torch.float32) if return_lse else None
-        _check(L.moe_cache4_attend(
-            self._c, q.data_ptr(), qs, tp, ts, n, lp, B, NHq, D ** -0.5 if scale is None else scale,
-            out.data_ptr(), os_, None if lse is None else lse.data_ptr(),
-            None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)), "moe_cache4_attend")
+        _check(lib().moe_cache4_attend(self._c, pack_attend(
+            q.data_ptr(), qs, tp, ts, lp, out.data_ptr(), os_, lse.data_ptr() if return_lse else 0,
+            ws.data_ptr() if nbytes else 0, nbytes, B, n, NHq, D ** -0.5 if scale is None else scale),
+            _raw_stream(dev)), "moe_cache4_attend")
         return (out, lse) if return_lse else out
 
 
@@ -627,7 +628,10 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     os_ = NHq * D
     if not fresh:
         os_ = _heads(out, "out", dev, (Tq, NHq, D))[3]
-        _no_overlap(out, (q, k, v), "out")
+        ospan = _span(out, Tq, NHq, D, os_)
+        _apart("out", ospan, _span(q, Tq, NHq, D, qs))
+        _apart("out", ospan, _span(k, Tk, NKV, D, ks))
+        _apart("out", ospan, _span(v, Tk, NKV, D, vs))
     if not _here(dev, stream):
         with _elsewhere(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out)):
             return prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, out, return_lse)
@@ -637,11 +641,11 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     if fresh:
         out = torch.empty_like(q)
     lse = q.new_empty((Tq, NHq), dtype=torch.float32) if return_lse else None
-    _check(lib().moe_prompt_attention(
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, B, Tq, Tk, NHq, NKV, D,
-        1 if causal else 0, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-        None if lse is None else lse.data_ptr(), 3 if fresh else 2,
-        None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev)), "moe_prompt_attention")
+    _check(lib().moe_prompt_attention(pack_prompt(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, out.data_ptr(), os_,
+        lse.data_ptr() if return_lse else 0, ws.data_ptr() if nbytes else 0, nbytes, Tq, Tk, B, NHq, NKV,
+        D, 1 if causal else 0, 3 if fresh else 2, D ** -0.5 if scale is None else scale),
+        _raw_stream(dev)), "moe_prompt_attention")
     return (out, lse) if return_lse else out
 
 

@@ -134,21 +134,23 @@ moe_status check_cache4(const moe_cache4* c) {
 Cache4 cache4_of(const moe_cache4& c) {
   return Cache4{static_cast<uint8_t*>(c.pages), c.num_pages, c.page_size / 16, c.NKV, c.D};
 }
-moe_status check_cache_places(const moe_cache4* c, const void* k, int64_t k_stride, const void* v,
-                              int64_t v_stride, const int32_t* table, int64_t table_stride,
-                              int32_t max_pages, const int32_t* start, const int32_t* cu, int32_t B,
-                              int64_t T) {
+CachePlaces places_of(const moe_cache4_tokens& t) {
+  return CachePlaces{t.block_table, t.table_stride, t.max_pages, t.start, t.cu_seqlens, t.B, t.T};
+}
+moe_status check_cache_tokens(const moe_cache4* c, const moe_cache4_tokens* t) {
   const moe_status st = check_cache4(c);
   if (st != MOE_OK) return st;
-  if (B < 0 || T < 0 || max_pages < 0 || table_stride < max_pages) return MOE_ERR_SHAPE;
-  if (!cu && T != B) return MOE_ERR_SHAPE;
-  if (T >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
-  if (!stride_ok(k_stride, c->NKV, c->D) || !stride_ok(v_stride, c->NKV, c->D))
+  if (!t) return MOE_ERR_NULL;
+  if (t->B < 0 || t->T < 0 || t->max_pages < 0 || t->table_stride < t->max_pages) return MOE_ERR_SHAPE;
+  if (!t->cu_seqlens && t->T != t->B) return MOE_ERR_SHAPE;
+  if (t->T >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(t->k_token_stride, c->NKV, c->D) || !stride_ok(t->v_token_stride, c->NKV, c->D))
     return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
-  if (!c->pages || !k || !v || (B > 0 && !start) || (B > 0 && max_pages > 0 && !table))
+  if (t->T == 0) return MOE_OK;
+  if (!c->pages || !t->k || !t->v || (t->B > 0 && !t->start) ||
+      (t->B > 0 && t->max_pages > 0 && !t->block_table))
     return MOE_ERR_NULL;
-  if (!aligned16(c->pages) || !aligned16(k) || !aligned16(v)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(c->pages) || !aligned16(t->k) || !aligned16(t->v)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 moe_status check_attend_shape(const moe_cache4* c, int32_t B, int32_t NHq, int32_t max_pages) {
@@ -674,31 +676,33 @@ moe_status moe_inv_rope_fp8_quant_per_head(const void* x, int64_t x_token_stride
                                           scales, num_cus(), stream));
 }
 
-moe_status moe_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                            const int64_t* positions, const float* cos_sin, int64_t max_pos,
-                            int64_t T, int32_t NHq, int32_t NHk, int32_t D, int32_t R,
-                            int32_t interleaved, const void* q_weight, const void* k_weight,
-                            int32_t weights_f32, float eps, void* q_out, int64_t q_out_stride,
-                            void* k_out, int64_t k_out_stride, hipStream_t stream) {
-  if (T < 0 || NHq <= 0 || NHk < 0 || D <= 0 || R <= 0 || max_pos <= 0) return MOE_ERR_SHAPE;
-  if (R > D || (R & 1)) return MOE_ERR_SHAPE;
-  if (D % 8 != 0 || D > 512) return MOE_ERR_UNSUPPORTED;
-  if (interleaved ? (R % 8 != 0) : (R % 16 != 0)) return MOE_ERR_UNSUPPORTED;
-  if (!(eps >= 0.0f && eps <= 3.0e38f)) return MOE_ERR_UNSUPPORTED;
-  if (!stride_ok(q_stride, NHq, D) || !stride_ok(q_out_stride, NHq, D)) return MOE_ERR_UNSUPPORTED;
-  if (NHk && (!stride_ok(k_stride, NHk, D) || !stride_ok(k_out_stride, NHk, D)))
+moe_status moe_qk_norm_rope(const moe_qk_norm_rope_args* a, hipStream_t stream) {
+  if (!a) return MOE_ERR_NULL;
+  if (a->T < 0 || a->NHq <= 0 || a->NHk < 0 || a->D <= 0 || a->R <= 0 || a->max_pos <= 0)
+    return MOE_ERR_SHAPE;
+  if (a->R > a->D || (a->R & 1)) return MOE_ERR_SHAPE;
+  if (a->D % 8 != 0 || a->D > 512) return MOE_ERR_UNSUPPORTED;
+  if (a->interleaved ? (a->R % 8 != 0) : (a->R % 16 != 0)) return MOE_ERR_UNSUPPORTED;
+  if (!(a->eps >= 0.0f && a->eps <= 3.0e38f)) return MOE_ERR_UNSUPPORTED;
+  const bool k = a->NHk != 0;
+  if (!stride_ok(a->q_token_stride, a->NHq, a->D) || !stride_ok(a->q_out_token_stride, a->NHq, a->D))
     return MOE_ERR_UNSUPPORTED;
-  if (T >= ((int64_t)1 << 32) / (NHq + (int64_t)NHk)) return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
-  if (!q || !positions || !cos_sin || !q_out || (NHk && (!k || !k_out))) return MOE_ERR_NULL;
-  if (!aligned16(q) || !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(q_weight) ||
-      (NHk && (!aligned16(k) || !aligned16(k_out) || !aligned16(k_weight))))
+  if (k && (!stride_ok(a->k_token_stride, a->NHk, a->D) ||
+            !stride_ok(a->k_out_token_stride, a->NHk, a->D)))
+    return MOE_ERR_UNSUPPORTED;
+  if (a->T >= ((int64_t)1 << 32) / (a->NHq + (int64_t)a->NHk)) return MOE_ERR_UNSUPPORTED;
+  if (a->T == 0) return MOE_OK;
+  if (!a->q || !a->positions || !a->cos_sin || !a->q_out || (k && (!a->k || !a->k_out)))
+    return MOE_ERR_NULL;
+  if (!aligned16(a->q) || !aligned16(a->q_out) || !aligned16(a->cos_sin) || !aligned16(a->q_weight) ||
+      (k && (!aligned16(a->k) || !aligned16(a->k_out) || !aligned16(a->k_weight))))
     return MOE_ERR_UNSUPPORTED;
   return guarded([&] {
-    const HeadRows qr{q, q_stride, q_out, q_out_stride, q_weight, NHq};
-    const HeadRows kr{k, k_stride, k_out, k_out_stride, NHk ? k_weight : nullptr, NHk};
-    return launch_qk_norm_rope(qr, kr, positions, cos_sin, max_pos, T, D, R, interleaved != 0,
-                               weights_f32 != 0, eps, num_cus(), stream);
+    const HeadRows qr{a->q, a->q_token_stride, a->q_out, a->q_out_token_stride, a->q_weight, a->NHq};
+    const HeadRows kr{a->k, a->k_token_stride, a->k_out, a->k_out_token_stride, k ? a->k_weight : nullptr,
+                      a->NHk};
+    return launch_qk_norm_rope(qr, kr, a->positions, a->cos_sin, a->max_pos, a->T, a->D, a->R,
+                               a->interleaved != 0, a->weights_f32 != 0, a->eps, num_cus(), stream);
   });
 }
 
@@ -707,31 +711,21 @@ size_t moe_cache4_page_bytes(int32_t page_size, int32_t NKV, int32_t D) {
   return (size_t)NKV * (page_size / 16) * 17 * D;
 }
 
-moe_status moe_cache4_write(const moe_cache4* cache, const void* k, int64_t k_stride,
-                            const void* v, int64_t v_stride, const int32_t* block_table,
-                            int64_t table_stride, int32_t max_pages, const int32_t* start,
-                            const int32_t* cu_seqlens, int32_t B, int64_t T, hipStream_t stream) {
-  const moe_status st = check_cache_places(cache, k, k_stride, v, v_stride, block_table,
-                                           table_stride, max_pages, start, cu_seqlens, B, T);
-  if (st != MOE_OK || T == 0) return st;
+moe_status moe_cache4_write(const moe_cache4* cache, const moe_cache4_tokens* t, hipStream_t stream) {
+  const moe_status st = check_cache_tokens(cache, t);
+  if (st != MOE_OK || t->T == 0) return st;
   return guarded([&] {
-    return launch_cache4_write(cache4_of(*cache),
-                               CachePlaces{block_table, table_stride, max_pages, start, cu_seqlens, B, T},
-                               k, k_stride, v, v_stride, stream);
+    return launch_cache4_write(cache4_of(*cache), places_of(*t), t->k, t->k_token_stride, t->v,
+                               t->v_token_stride, stream);
   });
 }
 
-moe_status moe_cache4_read(const moe_cache4* cache, void* k, int64_t k_stride, void* v,
-                           int64_t v_stride, const int32_t* block_table, int64_t table_stride,
-                           int32_t max_pages, const int32_t* start, const int32_t* cu_seqlens,
-                           int32_t B, int64_t T, int32_t zero_tail, hipStream_t stream) {
-  const moe_status st = check_cache_places(cache, k, k_stride, v, v_stride, block_table,
-                                           table_stride, max_pages, start, cu_seqlens, B, T);
-  if (st != MOE_OK || T == 0) return st;
+moe_status moe_cache4_read(const moe_cache4* cache, const moe_cache4_tokens* t, hipStream_t stream) {
+  const moe_status st = check_cache_tokens(cache, t);
+  if (st != MOE_OK || t->T == 0) return st;
   return guarded([&] {
-    return launch_cache4_read(cache4_of(*cache),
-                              CachePlaces{block_table, table_stride, max_pages, start, cu_seqlens, B, T},
-                              k, k_stride, v, v_stride, zero_tail != 0, stream);
+    return launch_cache4_read(cache4_of(*cache), places_of(*t), t->k, t->k_token_stride, t->v,
+                              t->v_token_stride, t->zero_tail != 0, stream);
   });
 }
 
@@ -743,28 +737,28 @@ size_t moe_cache4_attend_workspace_bytes(const moe_cache4* cache, int32_t B, int
   return cache4_attend_workspace(B, NHq, cache->D, splits);
 }
 
-moe_status moe_cache4_attend(const moe_cache4* cache, const void* q, int64_t q_stride,
-                             const int32_t* block_table, int64_t table_stride, int32_t max_pages,
-                             const int32_t* lens, int32_t B, int32_t NHq, float scale, void* out,
-                             int64_t out_stride, float* lse, void* workspace,
-                             size_t workspace_bytes, hipStream_t stream) {
-  const moe_status st = check_attend_shape(cache, B, NHq, max_pages);
+moe_status moe_cache4_attend(const moe_cache4* cache, const moe_cache4_attend_args* a,
+                             hipStream_t stream) {
+  if (!a) return MOE_ERR_NULL;
+  const moe_status st = check_attend_shape(cache, a->B, a->NHq, a->max_pages);
   if (st != MOE_OK) return st;
-  if (table_stride < max_pages) return MOE_ERR_SHAPE;
-  if (!scale_ok(scale)) return MOE_ERR_UNSUPPORTED;
-  if (!stride_ok(q_stride, NHq, cache->D) || !stride_ok(out_stride, NHq, cache->D))
+  if (a->table_stride < a->max_pages) return MOE_ERR_SHAPE;
+  if (!scale_ok(a->scale)) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(a->q_token_stride, a->NHq, cache->D) || !stride_ok(a->out_token_stride, a->NHq, cache->D))
     return MOE_ERR_UNSUPPORTED;
-  if (B == 0) return MOE_OK;
-  if (!cache->pages || !q || !lens || !out || (max_pages > 0 && !block_table)) return MOE_ERR_NULL;
-  if (!aligned16(cache->pages) || !aligned16(q) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
-  const int splits = cache4_attend_splits(B, NHq, cache->NKV, cache->D,
-                                          (int64_t)max_pages * cache->page_size);
-  const size_t need = cache4_attend_workspace(B, NHq, cache->D, splits);
-  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
-  if (need && !aligned16(workspace)) return MOE_ERR_UNSUPPORTED;
+  if (a->B == 0) return MOE_OK;
+  if (!cache->pages || !a->q || !a->lens || !a->out || (a->max_pages > 0 && !a->block_table))
+    return MOE_ERR_NULL;
+  if (!aligned16(cache->pages) || !aligned16(a->q) || !aligned16(a->out)) return MOE_ERR_UNSUPPORTED;
+  const int splits = cache4_attend_splits(a->B, a->NHq, cache->NKV, cache->D,
+                                          (int64_t)a->max_pages * cache->page_size);
+  const size_t need = cache4_attend_workspace(a->B, a->NHq, cache->D, splits);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need && !aligned16(a->workspace)) return MOE_ERR_UNSUPPORTED;
   return guarded([&] {
-    return launch_cache4_attend(cache4_of(*cache), q, q_stride, block_table, table_stride, max_pages,
-                                lens, B, NHq, scale, out, out_stride, lse, splits, workspace, stream);
+    return launch_cache4_attend(cache4_of(*cache), a->q, a->q_token_stride, a->block_table,
+                                a->table_stride, a->max_pages, a->lens, a->B, a->NHq, a->scale, a->out,
+                                a->out_token_stride, a->lse, splits, a->workspace, stream);
   });
 }
 
@@ -774,52 +768,50 @@ size_t moe_prompt_attention_workspace_bytes(int32_t B, int64_t Tq, int64_t Tk, i
   return prompt_workspace(Tq, NHq, D, prompt_splits(Tq, Tk, B, NHq, NKV, D));
 }
 
-moe_status moe_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                                const void* v, int64_t v_stride, const int32_t* cu_q,
-                                const int32_t* cu_k, int32_t B, int64_t Tq, int64_t Tk,
-                                int32_t NHq, int32_t NKV, int32_t D, int32_t causal, float scale,
-                                void* out, int64_t out_stride, float* lse, int32_t zero_tail,
-                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  const moe_status st = check_prompt_shape(B, Tq, Tk, NHq, NKV, D);
+moe_status moe_prompt_attention(const moe_prompt_attention_args* a, hipStream_t stream) {
+  if (!a) return MOE_ERR_NULL;
+  const moe_status st = check_prompt_shape(a->B, a->Tq, a->Tk, a->NHq, a->NKV, a->D);
   if (st != MOE_OK) return st;
-  if (!scale_ok(scale) || (zero_tail & ~3)) return MOE_ERR_UNSUPPORTED;
-  if (!stride_ok(q_stride, NHq, D) || !stride_ok(out_stride, NHq, D) ||
-      !stride_ok(k_stride, NKV, D) || !stride_ok(v_stride, NKV, D))
+  if (!scale_ok(a->scale) || (a->zero_tail & ~3)) return MOE_ERR_UNSUPPORTED;
+  if (!stride_ok(a->q_token_stride, a->NHq, a->D) || !stride_ok(a->out_token_stride, a->NHq, a->D) ||
+      !stride_ok(a->k_token_stride, a->NKV, a->D) || !stride_ok(a->v_token_stride, a->NKV, a->D))
     return MOE_ERR_UNSUPPORTED;
   // 32-bit byte offsets inside a tile of keys
-  if (k_stride > (1 << 24) || v_stride > (1 << 24)) return MOE_ERR_UNSUPPORTED;
-  if (Tq == 0) return MOE_OK;
-  if (B == 0 && !zero_tail) return MOE_OK;
-  if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !v))) return MOE_ERR_NULL;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return MOE_ERR_UNSUPPORTED;
-  const int splits = prompt_splits(Tq, Tk, B, NHq, NKV, D);
-  const size_t need = prompt_workspace(Tq, NHq, D, splits);
-  if (need && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
-  if (need && !aligned16(workspace)) return MOE_ERR_UNSUPPORTED;
+  if (a->k_token_stride > (1 << 24) || a->v_token_stride > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (a->Tq == 0) return MOE_OK;
+  if (a->B == 0 && !a->zero_tail) return MOE_OK;
+  if (!a->q || !a->cu_seqlens_q || !a->cu_seqlens_k || !a->out || (a->Tk > 0 && (!a->k || !a->v)))
+    return MOE_ERR_NULL;
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out))
+    return MOE_ERR_UNSUPPORTED;
+  const int splits = prompt_splits(a->Tq, a->Tk, a->B, a->NHq, a->NKV, a->D);
+  const size_t need = prompt_workspace(a->Tq, a->NHq, a->D, splits);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need && !aligned16(a->workspace)) return MOE_ERR_UNSUPPORTED;
   return guarded([&] {
     PromptArgs p{};
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k);
-    p.v = static_cast<const uint16_t*>(v);
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
-    p.out_stride = out_stride;
-    p.cu_q = cu_q;
-    p.cu_k = cu_k;
-    p.out = static_cast<uint16_t*>(out);
-    p.lse = lse;
-    p.Tq = Tq;
-    p.Tk = Tk;
-    p.B = B;
-    p.NHq = NHq;
-    p.NKV = NKV;
-    p.D = D;
-    p.causal = causal != 0;
-    p.zero_tail = zero_tail;
-    p.scale = scale;
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.k = static_cast<const uint16_t*>(a->k);
+    p.v = static_cast<const uint16_t*>(a->v);
+    p.q_stride = a->q_token_stride;
+    p.k_stride = a->k_token_stride;
+    p.v_stride = a->v_token_stride;
+    p.out_stride = a->out_token_stride;
+    p.cu_q = a->cu_seqlens_q;
+    p.cu_k = a->cu_seqlens_k;
+    p.out = static_cast<uint16_t*>(a->out);
+    p.lse = a->lse;
+    p.Tq = a->Tq;
+    p.Tk = a->Tk;
+    p.B = a->B;
+    p.NHq = a->NHq;
+    p.NKV = a->NKV;
+    p.D = a->D;
+    p.causal = a->causal != 0;
+    p.zero_tail = a->zero_tail;
+    p.scale = a->scale;
     p.splits = splits;
-    return launch_prompt_attention(p, workspace, stream);
+    return launch_prompt_attention(p, a->workspace, stream);
   });
 }
 

@@ -58,6 +58,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kStep = 32;                  // tokens of a wave's step
+constexpr int kJoinWaves = 16;
 constexpr int kMaxSplits = 128;
 constexpr int kOneSplit = 1024;            // tokens
 constexpr int kCols = 16;                  // query heads of a column tile
@@ -423,13 +424,14 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_attend_kernel(AttendArgs a
 }
 
 // Joins the splits of one head: a workgroup per (sequence, head), a lane for
-// every D / 64 features, the waves taking turns at the splits.  Sequences that
-// one split held are there already.
+// every D / 64 features, the waves (4, or 16 where there are many splits)
+// taking turns at the splits.  Sequences that one split held are there already.
 template <int D>
-__global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kJoinWaves * kWave) void cache4_join_kernel(AttendArgs a) {
   constexpr int kPer = D / kWave;              // features of a lane
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int waves = blockDim.x / kWave;
   const int64_t row = blockIdx.x;              // b * NHq + h
   const int b = (int)(row / a.NHq), h = (int)(row - (int64_t)b * a.NHq);
   int len;
@@ -457,13 +459,21 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttendArgs a) {
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.0f;
   const float* po = a.part_o + row * a.splits * D + lane * kPer;
-#pragma unroll 8
-  for (int s = wave; s < parts; s += kWaves) {
-    const float fs = __shfl(s < kWave ? f[0] : f[1], s & (kWave - 1));
+  for (int s0 = wave; s0 < parts; s0 += 4 * waves) {   // four loads under way
+    float x[4][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] += fs * po[(int64_t)s * D + k];
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) x[i][k] = po[(int64_t)min(s0 + i * waves, parts - 1) * D + k];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + i * waves;
+      const float fs = __shfl(s < kWave ? f[0] : f[1], s & (kWave - 1));
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += s < parts ? fs * x[i][k] : 0.0f;
+    }
   }
-  __shared__ float sum[kWaves][D];
+  __shared__ float sum[kJoinWaves][D];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) sum[wave][lane * kPer + k] = acc[k];
   __syncthreads();
@@ -471,8 +481,7 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttendArgs a) {
   const int d = threadIdx.x;
   if (d < D) {
     float o = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) o += sum[w][d];
+    for (int w = 0; w < waves; ++w) o += sum[w][d];
     (a.out + b * a.out_stride + (int64_t)h * D)[d] = (uint16_t)pack_bf16(o * scale, 0.0f);
   }
   if (d == 0 && a.lse) a.lse[row] = (top + __log2f(z)) * kLn2;
@@ -493,7 +502,8 @@ void launch_one(const AttendArgs& a, hipStream_t stream) {
   cache4_attend_kernel<D><<<grid, dim3(kThreads), attend_lds(D, a.G < kCols ? a.G : kCols),
                             stream>>>(a);
   if (a.splits > 1) {
-    cache4_join_kernel<D><<<dim3((unsigned)(a.B * a.NHq)), dim3(kThreads), 0, stream>>>(a);
+    cache4_join_kernel<D><<<dim3((unsigned)(a.B * a.NHq)),
+                            dim3(a.splits > 16 ? kJoinWaves * kWave : kThreads), 0, stream>>>(a);
   }
 }
 

@@ -683,11 +683,18 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a) {
 #pragma unroll
   for (int k = 0; k < kPer; ++k) o[k] = 0.0f;
   const float* po = a.part_o + at * a.splits * D + lane * kPer;
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float fs = __shfl(f, s);
+  for (int s0 = 0; s0 < parts; s0 += 4) {              // four loads under way
+    float x[4][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) o[k] = fmaf(fs, po[(int64_t)s * D + k], o[k]);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) x[i][k] = po[(int64_t)min(s0 + i, parts - 1) * D + k];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float fs = __shfl(f, (s0 + i) & (kWave - 1));
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o[k] += s0 + i < parts ? fs * x[i][k] : 0.0f;
+    }
   }
   store_row(a, true, token, h, 0, lane * kPer, o, m, l, lane == 0);
 }

@@ -2,6 +2,10 @@
 before any HIP call, so wrong calls are shown here without a GPU."""
 
 import ctypes
+import os
+import shutil
+import subprocess
+import tempfile
 
 import pytest
 import torch
@@ -9,6 +13,7 @@ import torch
 import moe_layer_05_amd as mm
 from moe_layer_05_amd import binding
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 OK, NULL, SHAPE, UNSUP, WS = 0, 1, 2, 3, 4
 P = 4096                       # a stand-in for an aligned device pointer; never read
 
@@ -19,10 +24,10 @@ def L():
 
 
 def norm_rope(L, **kw):
-    a = dict(q=P, qs=256, k=P, ks=128, pos=P, cs=P, max_pos=10, T=3, NHq=2, NHk=1, D=128, R=128,
-             inter=0, qw=P, kw=P, f32=0, eps=1e-6, qo=P, qos=256, ko=P, kos=128)
+    a = dict(q=P, qs=256, k=P, ks=128, pos=P, cs=P, max_pos=10, T=3, qw=P, kw=P, qo=P, qos=256, ko=P,
+             kos=128, NHq=2, NHk=1, D=128, R=128, inter=0, f32=0, eps=1e-6)
     a.update(kw)
-    return L.moe_qk_norm_rope(*a.values(), None)
+    return L.moe_qk_norm_rope(binding.pack_norm_rope(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -50,27 +55,27 @@ CACHES = [(dict(n=0), SHAPE), (dict(size=0), SHAPE), (dict(heads=0), SHAPE), (di
           (dict(n=1 << 31), UNSUP), (dict(heads=70000), UNSUP)]
 
 
-def places(fn, c, more=(), **kw):
-    a = dict(k=P, ks=256, v=P, vs=256, table=P, ts=5, pages=5, start=P, cu=P, B=2, T=9)
+def places(fn, c, **kw):
+    a = dict(k=P, ks=256, v=P, vs=256, table=P, ts=5, start=P, cu=P, T=9, B=2, pages=5, tail=0)
     a.update(kw)
-    return fn(c, *a.values(), *more, None)
+    return fn(c, binding.pack_tokens(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(pages=-1), SHAPE), (dict(ts=4), SHAPE),
-    (dict(cu=None), SHAPE), (dict(T=1 << 31), UNSUP), (dict(ks=128), UNSUP), (dict(vs=260), UNSUP),
-    (dict(k=None), NULL), (dict(v=None), NULL), (dict(table=None), NULL), (dict(start=None), NULL),
-    (dict(k=P + 2), UNSUP), (dict(v=P + 8), UNSUP), (dict(T=0), OK), (dict(T=0, B=0, cu=None), OK),
+    (dict(cu=0), SHAPE), (dict(T=1 << 31), UNSUP), (dict(ks=128), UNSUP), (dict(vs=260), UNSUP),
+    (dict(k=0), NULL), (dict(v=0), NULL), (dict(table=0), NULL), (dict(start=0), NULL),
+    (dict(k=P + 2), UNSUP), (dict(v=P + 8), UNSUP), (dict(T=0), OK), (dict(T=0, B=0, cu=0), OK),
 ])
 def test_cache_write_and_read(L, kw, want):
     assert places(L.moe_cache4_write, cache(), **kw) == want
-    assert places(L.moe_cache4_read, cache(), more=(0,), **kw) == want
+    assert places(L.moe_cache4_read, cache(), **kw) == want
 
 
 @pytest.mark.parametrize("c,want", CACHES + [(dict(pages=None), NULL), (dict(pages=P + 8), UNSUP)])
 def test_cache_shapes(L, c, want):
     assert places(L.moe_cache4_write, cache(**c)) == want
-    assert places(L.moe_cache4_read, cache(**c), more=(0,)) == want
+    assert places(L.moe_cache4_read, cache(**c)) == want
     if "D" not in c and "heads" not in c:
         assert attend(L, cache(**c)) == want
 
@@ -82,10 +87,10 @@ def test_cache_null(L):
 
 
 def attend(L, c, **kw):
-    a = dict(q=P, qs=512, table=P, ts=5, pages=5, lens=P, B=2, NHq=4, scale=0.1, out=P, os=512,
-             lse=None, ws=P, wsb=1 << 40)
+    a = dict(q=P, qs=512, table=P, ts=5, lens=P, out=P, os=512, lse=0, ws=P, wsb=1 << 40, B=2, pages=5,
+             NHq=4, scale=0.1)
     a.update(kw)
-    return L.moe_cache4_attend(c, *a.values(), None)
+    return L.moe_cache4_attend(c, binding.pack_attend(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -93,9 +98,9 @@ def attend(L, c, **kw):
     (dict(ts=4), SHAPE), (dict(B=70000), UNSUP), (dict(pages=(1 << 24) + 1, ts=1 << 30), UNSUP),
     (dict(scale=0.0), UNSUP), (dict(scale=-1.0), UNSUP), (dict(scale=float("nan")), UNSUP),
     (dict(scale=float("inf")), UNSUP), (dict(qs=384), UNSUP), (dict(os=516), UNSUP),
-    (dict(q=None), NULL), (dict(lens=None), NULL), (dict(out=None), NULL), (dict(table=None), NULL),
+    (dict(q=0), NULL), (dict(lens=0), NULL), (dict(out=0), NULL), (dict(table=0), NULL),
     (dict(q=P + 4), UNSUP), (dict(out=P + 8), UNSUP), (dict(B=0), OK),
-    (dict(pages=1000, ts=1000, ws=None), WS), (dict(pages=1000, ts=1000, wsb=16), WS),
+    (dict(pages=1000, ts=1000, ws=0), WS), (dict(pages=1000, ts=1000, wsb=16), WS),
     (dict(pages=1000, ts=1000, ws=P + 8), UNSUP),
 ])
 def test_attend(L, kw, want):
@@ -112,10 +117,10 @@ def test_attend_workspace(L):
 
 
 def prompt(L, **kw):
-    a = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cq=P, ck=P, B=2, Tq=9, Tk=9, NHq=4, NKV=2, D=128,
-             causal=1, scale=0.1, out=P, os=512, lse=None, tail=0, ws=None, wsb=0)
+    a = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cq=P, ck=P, out=P, os=512, lse=0, ws=0, wsb=0, Tq=9,
+             Tk=9, B=2, NHq=4, NKV=2, D=128, causal=1, tail=0, scale=0.1)
     a.update(kw)
-    return L.moe_prompt_attention(*a.values(), None)
+    return L.moe_prompt_attention(binding.pack_prompt(*a.values()), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -125,8 +130,8 @@ def prompt(L, **kw):
     (dict(Tq=1 << 30, NHq=128, qs=16384, os=16384), UNSUP), (dict(qs=384), UNSUP),
     (dict(ks=250), UNSUP), (dict(vs=128), UNSUP), (dict(os=513), UNSUP), (dict(tail=4), UNSUP),
     (dict(ks=(1 << 24) + 8), UNSUP), (dict(vs=1 << 30), UNSUP),
-    (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(cq=None), NULL),
-    (dict(ck=None), NULL), (dict(out=None), NULL), (dict(q=P + 8), UNSUP), (dict(v=P + 2), UNSUP),
+    (dict(q=0), NULL), (dict(k=0), NULL), (dict(v=0), NULL), (dict(cq=0), NULL),
+    (dict(ck=0), NULL), (dict(out=0), NULL), (dict(q=P + 8), UNSUP), (dict(v=P + 2), UNSUP),
     (dict(Tq=0), OK), (dict(B=0), OK), (dict(Tk=4096), WS), (dict(Tk=4096, ws=P, wsb=64), WS),
     (dict(Tk=4096, ws=P + 8, wsb=1 << 40), UNSUP),
 ])
@@ -157,7 +162,52 @@ def test_binding_refuses_host_tensors():
         mm.KVCache4(0, 16, 2, 128)
 
 
-def test_struct_layout():
+def test_null_arguments(L):
+    assert L.moe_qk_norm_rope(None, None) == NULL
+    assert L.moe_cache4_write(cache(), None, None) == NULL and L.moe_cache4_read(cache(), None, None) == NULL
+    assert L.moe_cache4_attend(cache(), None, None) == NULL and L.moe_prompt_attention(None, None) == NULL
+
+
+def test_struct_layouts_match_c():
+    """The packed bytes have the sizes and the offsets of the C structures."""
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    fields = {
+        "moe_cache4": "pages num_pages page_size NKV D",
+        "moe_qk_norm_rope_args": "q q_token_stride k k_token_stride positions cos_sin max_pos T q_weight k_weight "
+                                 "q_out q_out_token_stride k_out k_out_token_stride NHq NHk D R interleaved "
+                                 "weights_f32 eps",
+        "moe_cache4_tokens": "k k_token_stride v v_token_stride block_table table_stride start cu_seqlens T B "
+                             "max_pages zero_tail",
+        "moe_cache4_attend_args": "q q_token_stride block_table table_stride lens out out_token_stride lse workspace "
+                                  "workspace_bytes B max_pages NHq scale",
+        "moe_prompt_attention_args": "q q_token_stride k k_token_stride v v_token_stride cu_seqlens_q cu_seqlens_k "
+                                     "out out_token_stride lse workspace workspace_bytes Tq Tk B NHq NKV D causal "
+                                     "zero_tail scale",
+    }
+    prog = '#include <stdio.h>\n#include <stddef.h>\n#include "moe.h"\nint main(void) {\n'
+    for t, names in fields.items():
+        prog += f'  printf("%zu", sizeof({t}));\n'
+        prog += "".join(f'  printf(" %zu", offsetof({t}, {n}));\n' for n in names.split())
+        prog += '  printf("\\n");\n'
+    prog += "  return 0;\n}\n"
+    with tempfile.TemporaryDirectory() as d:
+        src, exe = os.path.join(d, "l.c"), os.path.join(d, "l")
+        open(src, "w").write(prog)
+        r = subprocess.run([gcc, "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", f"-I{ROOT}/include", src, "-o",
+                            exe], capture_output=True, text=True)
+        if r.returncode:
+            pytest.skip("cannot compile against hip_runtime_api.h: " + r.stderr[:200])
+        rows = [[int(v) for v in line.split()] for line in subprocess.check_output([exe], text=True).splitlines()]
     F = binding.Cache4
-    assert [getattr(F, n).offset for n, _ in F._fields_] == [0, 8, 16, 20, 24]
-    assert ctypes.sizeof(F) == 32
+    assert rows[0] == [ctypes.sizeof(F)] + [getattr(F, n).offset for n, _ in F._fields_]
+    packs = (binding.pack_norm_rope, binding.pack_tokens, binding.pack_attend, binding.pack_prompt)
+    for (t, names), row, pack in zip(list(fields.items())[1:], rows[1:], packs):
+        n = len(names.split())
+        zero = pack(*([0] * n))
+        assert len(zero) == row[0], t
+        for i in range(n):                       # field i alone is not zero from its offset on
+            one = pack(*[1 if j == i else 0 for j in range(n)])
+            at = [k for k in range(len(one)) if one[k]]
+            assert row[1 + i] <= at[0] < row[1 + i] + 4, (t, names.split()[i])
