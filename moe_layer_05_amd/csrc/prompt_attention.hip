@@ -19,29 +19,32 @@
 //    maximum, sum and rescaling need one exchange between the two halves and
 //    no LDS.  The V operand of the same keys, four keys of one feature per
 //    lane, comes from row-major V by the transposing LDS read.
-// Probabilities are rounded to bfloat16 for the second product (relative
-// 2^-9 each, random over the keys: the output's error stays at the size of its
-// own rounding); their sum is taken in float32 before that.  The running
+// Probabilities are rounded to bfloat16 for the second product (at most 2^-8
+// relative each, random over the keys: the output's error stays at the size of
+// its own rounding; a second bfloat16 for the rest, as the cache's attention
+// has it, would add half as many matrix instructions); their sum is taken in
+// float32 before that.  The running
 // maximum moves only when a score passes it by more than 8 (in powers of
 // two), so most tiles skip the rescaling of O^T.
 //
-// Work split: a workgroup of eight waves takes 256 query rows of one head, 32
-// rows a wave.  K and V tiles of 64 keys (32 for D = 192, 256) come to LDS by
-// direct loads into a ring of four, two tiles ahead; rows behind the last key
-// repeat it.  The two waves of a SIMD work in opposite phases (below): a
-// tile's two products are 32 matrix instructions (D = 128), its softmax about
-// 110 vector instructions of which 32 are exponentials, so neither may wait
-// for the other.  Each XCD takes a contiguous range of (head, tile) so that a
-// kv head's keys stay in one L2; inside a sequence the tiles with the most
-// keys go first.
+// Work split: a workgroup of eight waves takes 256 rows, 32 a wave, of one kv
+// head; a row is (query, head of the group), so that the heads of a group share
+// their keys and short prompts fill the rows.  K and V tiles of 64 keys (32 for
+// D = 192, 256) come to LDS by direct loads into a ring of four, two tiles
+// ahead; rows behind the last key repeat it.  The two waves of a SIMD work in
+// opposite phases (below): a tile's two products are 32 matrix instructions
+// (D = 128), its softmax about 110 vector instructions of which 32 are
+// exponentials, so neither may wait for the other.  Few query tiles over many keys split the keys; the parts go
+// to scratch in float32 and a second launch joins them.
 //
-// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 545 us = 1.01
-// PFLOP/s (D = 64, 192, 256: 0.72, 1.05, 1.12; not causal, D = 128: 1.11); a
-// library product of 8192^3 reaches 1.38 on the same card, the matrix
-// instructions of this kernel alone (no LDS reads, no softmax) 1.68.  Without
-// the softmax it takes 0.88 of its time, without the loads to LDS 0.94: what
-// bounds it is the phase of the products with its LDS reads (32 rows a wave:
-// one 16-byte read per matrix instruction).
+// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 508 us = 1.08
+// PFLOP/s (D = 64, 192, 256: 0.82, 1.14, 1.14; not causal, D = 128: 1.17); a
+// library product of 8192^3 reaches 1.38 on the same card.  In parts (not
+// causal, D = 128, before the values were read ahead: 975 us): without the
+// loads to LDS 905, without the softmax as well 858, without the LDS reads as
+// well 706, which is the matrix instructions and the barriers.  What bounds it
+// is the phase of the products: one wave of a SIMD at a time reads 1 KB of LDS
+// per matrix instruction, 128 bytes a cycle and compute unit.
 //
 // A key or value that a row does not see never reaches it: scores of masked
 // pairs are replaced, and a wave that ends with a value that is not finite
@@ -59,6 +62,7 @@ constexpr int kRows = 32;                       // rows of a wave
 constexpr int kBlockRows = 256;                 // rows of a workgroup
 constexpr int kMaxSplits = 64;
 constexpr int kLeast = 4;                       // tiles of keys of a split, at least
+constexpr int kWorth = 18;                      // tiles of keys from which splits are made
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
@@ -738,11 +742,15 @@ hipError_t prepare_prompt_kernels() {
 
 // Splits of the keys where the query tiles leave most of the 256 compute
 // units without work: as many as fill them, each with kLeast tiles if a
-// sequence had all the keys.
+// sequence had all the keys.  Below kWorth tiles of keys the second launch and
+// the float32 sums cost what the shorter chains give (one sequence, 16 heads
+// over 4 of 128: 512 tokens 20.2 us whole, 22.4 us split; 256 queries over 4096
+// keys 97 us whole, 30 us split).
 int prompt_splits(int64_t Tq, int64_t Tk, int64_t B, int NHq, int NKV, int D) {
   if (B == 0 || Tq == 0) return 1;
   const int64_t units = prompt_slots(Tq, B, NHq / NKV) * NKV;
-  const int64_t most = Tk / ((D <= 128 ? 64 : 32) * kLeast);
+  const int64_t tiles = Tk / (D <= 128 ? 64 : 32);
+  const int64_t most = tiles < kWorth ? 1 : tiles / kLeast;
   int64_t s = 256 / units;
   if (s > most) s = most;
   return (int)(s < 2 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
