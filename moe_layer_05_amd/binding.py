@@ -379,24 +379,24 @@ def _prompt_workspace(*shape):
     return lib().moe_prompt_attention_workspace_bytes(*shape)
 
 
-def _span(t, T, H, D, stride):
-    """The bytes [from, to) that heads [T, H, D] reach."""
-    p = t.data_ptr()
-    return p, p + 2 * ((T - 1) * stride + H * D) if T else p
+def _rows(t, T, n, stride):
+    """(address, rows, bytes of a row, bytes from row to row) of T rows of n
+    bfloat16."""
+    return t.data_ptr(), T, 2 * n, 2 * stride
 
 
 def _apart(name, a, b):
-    """Refuses an output whose span meets an input's."""
-    if a[0] < b[1] and b[0] < a[1]:
-        raise ValueError(f"{name} must not overlap an input")
-
-
-def _inner_out(y, x, T, H, D, stride, name, dev):
-    """The token stride of an output that may be its input itself."""
-    ys = _heads(y, name, dev, (T, H, D))[3]
-    if y.data_ptr() != x.data_ptr() or ys != stride:
-        _apart(name, _span(y, T, H, D, ys), _span(x, T, H, D, stride))
-    return ys
+    """Refuses an output whose memory meets an input's (rows as _rows gives
+    them).  Rows of the same pitch may lie between each other, as the parts of
+    a fused projection do."""
+    (p, n, row, pitch), (p2, n2, row2, pitch2) = a, b
+    if not n or not n2 or p >= p2 + (n2 - 1) * pitch2 + row2 or p2 >= p + (n - 1) * pitch + row:
+        return
+    if pitch == pitch2:
+        d = (p2 - p) % pitch
+        if d >= row and d + row2 <= pitch:
+            return
+    raise ValueError(f"{name} must not overlap an input")
 
 
 def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=1e-6,
@@ -410,7 +410,7 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
     inputs otherwise."""
     T, NHq, D, qs = _heads(q, "q")
     dev = q.get_device()
-    NHk = ks = kos = kp = kop = f32 = qw = kw = 0
+    NHk = ks = kp = kop = f32 = qw = kw = 0
     if k is not None:
         Tk, NHk, Dk, ks = _heads(k, "k", dev)
         if Tk != T or Dk != D:
@@ -431,9 +431,21 @@ def qk_norm_rope(q, k, positions, cos_sin, R, q_weight=None, k_weight=None, eps=
             qw = _vector(q_weight, wt, D, "q_weight", dev)
         if k_weight is not None:
             kw = _vector(k_weight, wt, D, "k_weight", dev)
-    qos = NHq * D if q_out is None else _inner_out(q_out, q, T, NHq, D, qs, "q_out", dev)
-    if k is not None:
-        kos = NHk * D if k_out is None else _inner_out(k_out, k, T, NHk, D, ks, "k_out", dev)
+    qos, kos = NHq * D, NHk * D
+    if q_out is not None or k_out is not None:
+        qr, kr = _rows(q, T, NHq * D, qs), _rows(k, T, NHk * D, ks) if NHk else (0, 0, 0, 0)
+        if q_out is not None:
+            qos = _heads(q_out, "q_out", dev, (T, NHq, D))[3]
+            out = _rows(q_out, T, NHq * D, qos)
+            if out != qr:
+                _apart("q_out", out, qr)
+            _apart("q_out", out, kr)
+        if k_out is not None:
+            kos = _heads(k_out, "k_out", dev, (T, NHk, D))[3]
+            out = _rows(k_out, T, NHk * D, kos)
+            if out != kr:
+                _apart("k_out", out, kr)
+            _apart("k_out", out, qr)
     if not _here(dev, stream):
         with _elsewhere(dev, stream, (q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out)):
             return qk_norm_rope(q, k, positions, cos_sin, R, q_weight, k_weight, eps, interleaved, q_out, k_out)
@@ -486,7 +498,7 @@ class KVCache4:
         self.pages = pages
         self.num_pages, self.NKV, self.page_size, self.D = n, NKV, 16 * tiles, row // 17
         self._dev = pages.get_device()
-        self._span = pages.data_ptr(), pages.data_ptr() + pages.numel()
+        self._rows = pages.data_ptr(), 1, pages.numel(), pages.numel()
         self._c = ctypes.byref(Cache4(pages.data_ptr(), n, NKV=NKV, page_size=16 * tiles, D=row // 17))
 
     def _table(self, t, B):
@@ -548,11 +560,10 @@ class KVCache4:
         ks = vs = self.NKV * self.D
         if not fresh:
             ks, vs = _heads(k, "k", self._dev, shape)[3], _heads(v, "v", self._dev, shape)[3]
-            kspan, vspan = _span(k, *shape, ks), _span(v, *shape, vs)
-            _apart("k", kspan, self._span)
-            _apart("v", vspan, self._span)
-            if k.data_ptr() == v.data_ptr() or ks == self.NKV * self.D == vs:
-                _apart("k", kspan, vspan)        # (interleaved rows of one tensor are told apart)
+            kr, vr = _rows(k, T, self.NKV * self.D, ks), _rows(v, T, self.NKV * self.D, vs)
+            _apart("k", kr, vr)
+            _apart("k", kr, self._rows)
+            _apart("v", vr, self._rows)
         if not _here(self._dev, stream):
             with _elsewhere(self._dev, stream, (self.pages, block_table, start, cu_seqlens, k, v)):
                 return self.read(block_table, start, cu_seqlens, T, k, v)
@@ -580,9 +591,9 @@ class KVCache4:
         os_ = NHq * D
         if out is not None:
             os_ = _heads(out, "out", dev, (B, NHq, D))[3]
-            ospan = _span(out, B, NHq, D, os_)
-            _apart("out", ospan, _span(q, B, NHq, D, qs))
-            _apart("out", ospan, self._span)
+            rows = _rows(out, B, NHq * D, os_)
+            _apart("out", rows, _rows(q, B, NHq * D, qs))
+            _apart("out", rows, self._rows)
         if not _here(dev, stream):
             with _elsewhere(dev, stream, (self.pages, q, block_table, lens, out)):
                 return self.attend(q, block_table, lens, scale, out, return_lse)
@@ -628,10 +639,10 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     os_ = NHq * D
     if not fresh:
         os_ = _heads(out, "out", dev, (Tq, NHq, D))[3]
-        ospan = _span(out, Tq, NHq, D, os_)
-        _apart("out", ospan, _span(q, Tq, NHq, D, qs))
-        _apart("out", ospan, _span(k, Tk, NKV, D, ks))
-        _apart("out", ospan, _span(v, Tk, NKV, D, vs))
+        rows = _rows(out, Tq, NHq * D, os_)
+        _apart("out", rows, _rows(q, Tq, NHq * D, qs))
+        _apart("out", rows, _rows(k, Tk, NKV * D, ks))
+        _apart("out", rows, _rows(v, Tk, NKV * D, vs))
     if not _here(dev, stream):
         with _elsewhere(dev, stream, (q, k, v, cu_seqlens, cu_seqlens_k, out)):
             return prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, out, return_lse)

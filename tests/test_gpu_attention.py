@@ -225,6 +225,21 @@ def test_cache_every_bfloat16():
     assert np.array_equal(f64(v)[:, 0], want[::-1], equal_nan=True)
 
 
+def test_cache_reads_into_parts_of_rows():
+    """k and v as the two parts of the rows of one tensor."""
+    say("cache into parts")
+    g = gen(9)
+    D, NKV, n = 64, 2, 20
+    k, v = normal(g, n, NKV, D).to(DEV), normal(g, n, NKV, D).to(DEV)
+    c, tab = mm.KVCache4(2, 16, NKV, D), i32([[1, 0]])
+    c.write(k, v, tab, i32([0]), i32([0, n]))
+    a, b = c.read(tab, i32([0]), i32([0, n]), n)
+    rows = torch.full((n, 3 * NKV * D), 5.0, dtype=torch.bfloat16, device=DEV)
+    parts = rows.view(n, 3, NKV, D)
+    c.read(tab, i32([0]), i32([0, n]), n, k=parts[:, 0], v=parts[:, 2])
+    assert torch.equal(parts[:, 0], a) and torch.equal(parts[:, 2], b) and (parts[:, 1] == 5.0).all()
+
+
 def test_cache_skips_what_has_no_place():
     """Negative starts, positions behind the table, page ids outside the
     cache: nothing is written there and zeros are read; rows behind the last
@@ -699,6 +714,7 @@ def test_binding_refusals():
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device=DEV)
     pos = torch.zeros(4, dtype=torch.int64, device=DEV)
     cs = torch.zeros(8, 64, device=DEV)
+    x2, wide = torch.zeros_like(x), torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
     c = mm.KVCache4(3, 16, 2, 64)
     tab, one = torch.zeros(4, 1, dtype=torch.int32, device=DEV), i32([0, 0, 0, 0])
     wrong = [
@@ -712,6 +728,10 @@ def test_binding_refusals():
         lambda: mm.qk_norm_rope(x, None, pos, cs, 64, None, torch.ones(64, device=DEV)),
         lambda: mm.qk_norm_rope(x.transpose(1, 2), None, pos, cs, 64),
         lambda: mm.qk_norm_rope(x[1:], None, pos[1:], cs, 64, q_out=x[:3]),
+        lambda: mm.qk_norm_rope(x, x2, pos, cs, 64, q_out=x2),
+        lambda: mm.qk_norm_rope(x, x2, pos, cs, 64, k_out=x),
+        lambda: c.read(tab, one, None, 4, k=x, v=x),
+        lambda: c.read(tab, one, None, 4, k=wide[:, :128].view(4, 2, 64), v=wide[:, 64:192].view(4, 2, 64)),
         lambda: c.write(x, x[:3], tab, one),
         lambda: c.write(x[:3], x[:3], tab, one),
         lambda: c.write(x, x, tab.long(), one),
