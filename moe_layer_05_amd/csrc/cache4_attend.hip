@@ -9,7 +9,7 @@
 // 4 * D operations per query head, so up to 16 query heads share a column
 // tile.  The stream leaves a compute unit 13 cycles a token (D = 128, 5.2
 // TB/s): per 32 tokens a wave reads four 16-byte pieces per lane and issues
-// about 270 instructions, which several waves per SIMD have to overlap.
+// about 300 instructions, which several waves per SIMD have to overlap.
 //
 // A wave takes steps of 32 tokens (two tiles of 16).  Both products run on
 // 16x16x32 bfloat16 matrix instructions; E2M1 times a power of two is exact
@@ -46,10 +46,15 @@
 // scratch in float32 and a second launch joins them.  Page ids come 64 at a
 // time into a register, so that a step's loads wait for no other load.
 //
-// Measured (both launches): one sequence of 131072 tokens, 64 heads over 8 of
-// 128: 36 us = 3.9 TB/s of cache; 64 sequences of up to 8192, 32 heads over 4:
-// 43 us = 3.6 TB/s; 4 of up to 300, 16 over 2: 5.3 us.  Page ids loaded when a
-// step needed them: 60 us for the first.
+// Measured (both launches, caches in turn so that they come from HBM): one
+// sequence of 131072 tokens, 64 heads over 8 of 128: 34 us = 4.2 TB/s of cache;
+// 64 sequences of up to 8192, 32 heads over 4: 47 us = 3.3 TB/s (the second
+// bfloat16 of the probabilities is 4 us of it); 4 of up to 300, 16 over 2: 5.4
+// us.  Page ids loaded when a step needed them: 60 us for the first.  Equal
+// shares of all sequences' steps behind each other in place of equal parts of
+// each: 44 us for the second, but 12.3 against 9.7 us for 4 sequences of up to
+// 4000 and 17.6 against 11.3 us for 64 of up to 2048 with one kv head, since the
+// prefix sum over lens and the change of sequence stand in the way of the loads.
 #include "cache4_device.hpp"
 
 namespace moe {
@@ -520,12 +525,13 @@ hipError_t prepare_cache4_attend_kernels() {
 // Splits that a sequence may have.  Few sequences: as many as make one round
 // of resident workgroups (256 compute units, 4, 3 or 2 workgroups each by the
 // registers of the head size; one sequence of 131072 tokens, 8 kv heads of
-// 128: 96 splits 36 us, 128 splits, a round and a third, 42 us).  Sixteen and
-// more: their lengths differ, and shorter splits even them out (64 sequences
-// of up to 8192, 4 kv heads: 3 splits 48 us, 6 splits 43 us).  At most as many
-// as have kLeast steps each when the sequences are as long as the table
-// allows; one, and one launch, for tables of up to kOneSplit tokens (4
-// sequences of up to 300 tokens: 5.3 us against 7.4 us with a second launch).
+// 128: 64 splits 36.1 us, 96 splits 35.2 us, 128 splits, a round and a third,
+// 38.0 us).  Sixteen and more: their lengths differ, and shorter splits even
+// them out (64 sequences of up to 8192, 4 kv heads: 3 splits 51.6 us, 4 splits
+// 48.6 us, 6 splits 47.6 us, 8 splits 49.0 us).  At most as many as have kLeast
+// steps each when the sequences are as long as the table allows; one, and one
+// launch, for tables of up to kOneSplit tokens (4 sequences of up to 300 tokens:
+// 5.5 us against 7.9 us with a second launch).
 int cache4_attend_splits(int64_t B, int NHq, int NKV, int D, int64_t capacity) {
   const int64_t units = B * NKV * ((NHq / NKV + kCols - 1) / kCols);
   const int64_t round = 256 * (D == 64 ? 4 : (D == 128 ? 3 : 2));

@@ -37,14 +37,16 @@
 // exponentials, so neither may wait for the other.  Few query tiles over many keys split the keys; the parts go
 // to scratch in float32 and a second launch joins them.
 //
-// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 508 us = 1.08
-// PFLOP/s (D = 64, 192, 256: 0.82, 1.14, 1.14; not causal, D = 128: 1.17); a
+// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 517 us = 1.06
+// PFLOP/s (D = 64, 192, 256: 0.79, 1.10, 1.11; not causal, D = 128: 1.15); a
 // library product of 8192^3 reaches 1.38 on the same card.  In parts (not
 // causal, D = 128, before the values were read ahead: 975 us): without the
 // loads to LDS 905, without the softmax as well 858, without the LDS reads as
 // well 706, which is the matrix instructions and the barriers.  What bounds it
 // is the phase of the products: one wave of a SIMD at a time reads 1 KB of LDS
-// per matrix instruction, 128 bytes a cycle and compute unit.
+// per matrix instruction, 128 bytes a cycle and compute unit.  A
+// tile takes 3300 cycles (2048 of matrix instructions), at a clock that falls to
+// 1.5 .. 1.9 GHz under this load.
 //
 // A key or value that a row does not see never reaches it: scores of masked
 // pairs are replaced, and a wave that ends with a value that is not finite
