@@ -28,7 +28,7 @@
 // two), so most tiles skip the rescaling of O^T.
 //
 // Work split: a workgroup of eight waves takes 256 rows, 32 a wave, of one kv
-// head; a row is (query, head of the group), so that the heads of a group share
+// head (of four waves 128, where that gives all compute units work); a row is (query, head of the group), so that the heads of a group share
 // their keys and short prompts fill the rows.  K and V tiles of 64 keys (32 for
 // D = 192, 256) come to LDS by direct loads into a ring of four, two tiles
 // ahead; rows behind the last key repeat it.  The two waves of a SIMD work in
@@ -61,7 +61,6 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 32;                       // rows of a wave
-constexpr int kBlockRows = 256;                 // rows of a workgroup
 constexpr int kMaxSplits = 64;
 constexpr int kLeast = 4;                       // tiles of keys of a split, at least
 constexpr int kWorth = 18;                      // tiles of keys from which splits are made
@@ -80,6 +79,7 @@ struct Shape {
   static constexpr int D = D_, kWaves = WAVES_, kBufs = BUFS_;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int kBlockRows = kWaves * kRows;
+  static constexpr bool kPaired = kWaves == 8;            // two waves on a SIMD, in opposite phases
   // keys of a tile
   static constexpr int KB = D <= 128 ? 64 : 32;
   static constexpr int kRowBytes = 2 * D;
@@ -95,7 +95,7 @@ struct Shape {
   // value operands read during the softmax
   static constexpr int kPre = D == 128 ? 8 : (D == 192 ? 2 : 0);
   // D = 64: two workgroups to a compute unit
-  static constexpr int kWavesPerSimd = D == 64 ? 4 : 2;
+  static constexpr int kWavesPerSimd = D == 64 && kPaired ? 4 : 2;
   // The 16-byte pieces of a row are XOR-ed with a function of the row inside
   // groups of kGroup.  The 64 banks hold 256 bytes: rows of 256 or 512 bytes
   // all start at the same bank; 16 rows that read the same piece need 16
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   // Where a wave's loads of K fall on whole rounds of the waves, they differ by
   // whole rows that leave the XOR as it is: one offset does for all of them,
   // and one for those of V.
-  constexpr bool kEven = S::kHalf / 1024 % S::kWaves == 0;
+  constexpr bool kEven = S::kHalf / 1024 % S::kWaves == 0 && 1024 % S::kRowBytes == 0;
   constexpr int kHalfLoads = S::kLoads / 2;
   static_assert(!kEven || S::kWaves * kRowsOfLoad % 16 == 0, "rows of a round");
   auto load_is_v = [&](int i) { return kEven ? i >= kHalfLoads : wave + i * S::kWaves >= S::kHalf / 1024; };
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     asm volatile("" : "+v"(l));
   };
 
-  // Phases.  A wave alternates between matrix products (the scores of tile t
+  // Phases (kPaired).  A wave alternates between matrix products (the scores of tile t
   // and the values of tile t - 1) and the softmax of tile t; the second half
   // of the waves is one phase behind the first, so that on every SIMD one wave
   // multiplies while the other takes exponentials.  A barrier ends each phase.
@@ -554,7 +554,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   // half: before the softmax of tile t - 1) every wave's loads of tile t have
   // arrived; after it the last reader of tile t - 2 (the second half's
   // products of tile t - 1) is done, and its buffer takes tile t + kBufs - 2.
-  const bool late = wave >= S::kWaves / 2;
+  // Four waves have a SIMD each and no opposite phase: the odd barriers fall
+  // away, and the same holds of the even ones.
+  const bool late = S::kPaired && wave >= S::kWaves / 2;
   auto even = [&](int t) {
     if (t + S::kAhead <= tiles) wait_loads<(S::kAhead - 1) * S::kLoads>();
     else wait_loads<0>();
@@ -569,7 +571,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
   auto before_softmax = [&](int t) {
     if (late) even(t + 1);
-    else barrier();
+    else if (S::kPaired) barrier();
   };
   auto after_softmax = [&](int t) {
     if (late) barrier();
@@ -598,7 +600,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     before_softmax(t);
     after_softmax(t);
   }
-  if (!late) barrier();                                // the second half's last products
+  if (S::kPaired && !late) barrier();                  // the second half's last products
 
   float odd = 0.0f;                                    // NaN as soon as one value is not finite
 #pragma unroll
@@ -705,40 +707,59 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a) {
   store_row(a, true, token, h, 0, lane * kPer, o, m, l, lane == 0);
 }
 
-template <typename S>
-hipError_t prepare_one() {
-  hipError_t e = prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<S>), S::kLds);
-  if (e == hipSuccess) e = prepare_kernel(reinterpret_cast<const void*>(&prompt_join_kernel<S>), 0);
-  return e;
-}
-
 // Each sequence ends with at most one part tile.
-int64_t prompt_slots(int64_t Tq, int64_t B, int G) { return Tq * G / kBlockRows + B; }
+int64_t prompt_slots(int64_t Tq, int64_t B, int G, int rows) { return Tq * G / rows + B; }
 
 template <typename S>
 void launch_one(const PromptArgs& p, hipStream_t stream) {
-  static_assert(S::kBlockRows == kBlockRows, "rows of a workgroup");
   // one slot more, so that some slot is left for the rows behind the last sequence
-  const int64_t slots = prompt_slots(p.Tq, p.B, p.NHq / p.NKV) + (p.zero_tail ? 1 : 0);
+  const int64_t slots = prompt_slots(p.Tq, p.B, p.NHq / p.NKV, S::kBlockRows) + (p.zero_tail ? 1 : 0);
   const int64_t groups = slots * p.NKV * p.splits;
   prompt_attention_kernel<S><<<dim3((unsigned)((groups + 7) / 8 * 8)), dim3(S::kThreads), S::kLds, stream>>>(
       p, (int)slots);
-  if (p.splits > 1)
-    prompt_join_kernel<S><<<dim3((unsigned)((p.Tq * p.NHq + 3) / 4)), dim3(256), 0, stream>>>(p);
 }
 
-typedef Shape<64, 8, 4> S64;
-typedef Shape<128, 8, 4> S128;
-typedef Shape<192, 8, 4> S192;
-typedef Shape<256, 8, 4> S256;
+template <int D>
+using Pairs = Shape<D, 8, 4>;                          // 256 rows
+template <int D>
+using Fours = Shape<D, 4, 4>;                          // 128 rows
+
+template <int D>
+hipError_t prepare_head() {
+  hipError_t e = prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<Pairs<D>>), Pairs<D>::kLds);
+  if (e == hipSuccess) e = prepare_kernel(reinterpret_cast<const void*>(&prompt_join_kernel<Pairs<D>>), 0);
+  if constexpr (D < 256)
+    if (e == hipSuccess)
+      e = prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<Fours<D>>), Fours<D>::kLds);
+  return e;
+}
+
+// Workgroups of four waves where the keys are whole and the rows leave them in
+// one round of 256 compute units (two each at D = 64): a compute unit then has
+// less of them, and a wave that has its SIMD to itself goes through a tile
+// without waiting for the other's phase.  Four against eight waves: 100 tokens,
+// 16 heads over 2 of 128, 8.7 and 11.2 us; 1024 tokens, 16 over 4, 27.3 and 31.4
+// us; 2048 tokens 49.1 and 56.1 us, D = 64 31.1 and 38.7 us; where they do not
+// fit one round, 8 x 1024 tokens, 81 and 68 us (D = 64 the same).  Not at D =
+// 256: 1024 tokens, 8 heads over 2, 41 and 37 us (it spills).
+template <int D>
+void launch_head(const PromptArgs& p, hipStream_t stream) {
+  if constexpr (D < 256) {
+    if (p.splits == 1 && p.Tq * p.NHq <= (D == 64 ? 512 : 256) * Fours<D>::kBlockRows)
+      return launch_one<Fours<D>>(p, stream);
+  }
+  launch_one<Pairs<D>>(p, stream);
+  if (p.splits > 1)
+    prompt_join_kernel<Pairs<D>><<<dim3((unsigned)((p.Tq * p.NHq + 3) / 4)), dim3(256), 0, stream>>>(p);
+}
 
 }  // namespace
 
 hipError_t prepare_prompt_kernels() {
-  hipError_t e = prepare_one<S64>();
-  if (e == hipSuccess) e = prepare_one<S128>();
-  if (e == hipSuccess) e = prepare_one<S192>();
-  if (e == hipSuccess) e = prepare_one<S256>();
+  hipError_t e = prepare_head<64>();
+  if (e == hipSuccess) e = prepare_head<128>();
+  if (e == hipSuccess) e = prepare_head<192>();
+  if (e == hipSuccess) e = prepare_head<256>();
   return e;
 }
 
@@ -746,11 +767,11 @@ hipError_t prepare_prompt_kernels() {
 // units without work: as many as fill them, each with kLeast tiles if a
 // sequence had all the keys.  Below kWorth tiles of keys the second launch and
 // the float32 sums cost what the shorter chains give (one sequence, 16 heads
-// over 4 of 128: 512 tokens 20.2 us whole, 22.4 us split; 256 queries over 4096
+// over 4 of 128: 512 tokens 16.3 us whole, 22.4 us split; 256 queries over 4096
 // keys 97 us whole, 30 us split).
 int prompt_splits(int64_t Tq, int64_t Tk, int64_t B, int NHq, int NKV, int D) {
   if (B == 0 || Tq == 0) return 1;
-  const int64_t units = prompt_slots(Tq, B, NHq / NKV) * NKV;
+  const int64_t units = prompt_slots(Tq, B, NHq / NKV, Pairs<64>::kBlockRows) * NKV;
   const int64_t tiles = Tk / (D <= 128 ? 64 : 32);
   const int64_t most = tiles < kWorth ? 1 : tiles / kLeast;
   int64_t s = 256 / units;
@@ -768,10 +789,10 @@ hipError_t launch_prompt_attention(PromptArgs p, void* workspace, hipStream_t st
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)p.Tq * p.NHq * p.splits * p.D);
   switch (p.D) {
-    case 64: launch_one<S64>(p, stream); break;
-    case 128: launch_one<S128>(p, stream); break;
-    case 192: launch_one<S192>(p, stream); break;
-    default: launch_one<S256>(p, stream); break;
+    case 64: launch_head<64>(p, stream); break;
+    case 128: launch_head<128>(p, stream); break;
+    case 192: launch_head<192>(p, stream); break;
+    default: launch_head<256>(p, stream); break;
   }
   return hipGetLastError();
 }
