@@ -467,7 +467,7 @@ size_t moe_cache4_page_bytes(int32_t page_size, int32_t NKV, int32_t D);
  *   start        [B] int32
  *   cu_seqlens   [B + 1] int32, or NULL: one token per sequence (T == B)
  *   zero_tail    moe_cache4_read: != 0 zeroes the rows of k and v behind the
- *                last sequence
+ *                last sequence (and before the first)
  */
 typedef struct {
   void* k;
@@ -551,8 +551,9 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const moe_cache4_attend_ar
  *   cu_seqlens_q, cu_seqlens_k   [B + 1] int32
  *   out           [Tq][NHq][D] bfloat16 (out), 16-byte aligned
  *   lse           [Tq][NHq] float32 (out), or NULL
- *   zero_tail     bit 0: rows of out behind the last sequence become 0, bit 1:
- *                 rows of lse behind it become -inf
+ *   zero_tail     bit 0: rows of out that no sequence has (behind the last, or
+ *                 before the first where cu_seqlens_q[0] > 0) become 0, bit 1:
+ *                 such rows of lse become -inf
  *   workspace     >= moe_prompt_attention_workspace_bytes(...) device bytes,
  *                 16-byte aligned; NULL where that is 0.  Calls that may
  *                 overlap, graphs included, need workspaces of their own.

@@ -619,8 +619,8 @@ def prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, scale=
     causal: its last query sees its last key.  Scores are scaled by ``scale``
     (default 1 / sqrt(D)).  With ``return_lse`` (out, lse), lse [Tq, NHq]
     float32.  A query that sees nothing gives zeros and -inf.  Rows behind the
-    last sequence are left as they were in a given ``out``, zero in a new one
-    and -inf in lse."""
+    last sequence (and before the first) are left as they were in a given
+    ``out``, zero in a new one and -inf in lse."""
     Tq, NHq, D, qs = _heads(q, "q")
     dev = q.get_device()
     Tk, NKV, Dk, ks = _heads(k, "k", dev)

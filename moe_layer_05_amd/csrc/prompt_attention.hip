@@ -289,16 +289,19 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   }
   seq = __builtin_amdgcn_readfirstlane(seq);
   if (seq < 0) {
-    // no tile: such slots share the rows behind the last sequence
+    // no tile: such slots share the rows behind the last sequence and before
+    // the first
     if (split > 0) return;
-    int64_t behind = a.cu_q[a.B];
-    behind = behind < 0 ? 0 : behind;
-    for (int64_t t = behind + (x - total); t < a.Tq; t += slots - total) {
+    int64_t before = a.cu_q[0], behind = a.cu_q[a.B];
+    before = before < 0 ? 0 : (before > a.Tq ? a.Tq : before);
+    behind = behind < before ? before : (behind > a.Tq ? a.Tq : behind);
+    for (int64_t i = x - total; i < before + (a.Tq - behind); i += slots - total) {
+      const int64_t t = i < before ? i : behind + (i - before);
       if (a.zero_tail & 1)
-        for (int i = tid; i < G * (D / 8); i += S::kThreads)
-          reinterpret_cast<uint4*>(a.out + t * a.out_stride + (int64_t)kvh * G * D)[i] = make_uint4(0, 0, 0, 0);
+        for (int j = tid; j < G * (D / 8); j += S::kThreads)
+          reinterpret_cast<uint4*>(a.out + t * a.out_stride + (int64_t)kvh * G * D)[j] = make_uint4(0, 0, 0, 0);
       if ((a.zero_tail & 2) && a.lse)
-        for (int i = tid; i < G; i += S::kThreads) a.lse[t * a.NHq + kvh * G + i] = kNegInf;
+        for (int j = tid; j < G; j += S::kThreads) a.lse[t * a.NHq + kvh * G + j] = kNegInf;
     }
     return;
   }

@@ -545,6 +545,26 @@ def test_prompt_strides_and_tail():
     assert (wide[T:] == 3.0).all() and (wide[:, :NHq * D] == 3.0).all()
 
 
+@pytest.mark.parametrize("T,first", [(300, 40), (300, 300), (30000, 500)])
+def test_prompt_rows_before_the_first_sequence(T, first):
+    """A batch whose first sequence starts behind row 0: the rows before it
+    are like those behind the last one."""
+    say("prompt rows before", T, first)
+    g = gen(T + first)
+    D, NHq, NKV, n = 64, 4, 2, min(70, T - first)
+    q, k, v = (normal(g, T, h, D) for h in (NHq, NKV, NKV))
+    at = i32([first, first + n])
+    out, lse = mm.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), at, return_lse=True)
+    mine = slice(first, first + n)
+    check_prompt(out[mine], lse[mine], q[mine], k[mine], v[mine], [n], [n], True, D ** -0.5)
+    free = torch.ones(T, dtype=torch.bool, device=DEV)
+    free[mine] = False
+    assert not out[free].any() and torch.isneginf(lse[free]).all()
+    given = torch.full_like(out, 3.0)
+    mm.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), at, out=given)
+    assert torch.equal(given[mine], out[mine]) and (given[free] == 3.0).all()
+
+
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
 @pytest.mark.parametrize("what", ["nan", "inf"])
 def test_prompt_future_tokens_stay_out(D, what):
