@@ -402,7 +402,9 @@ moe_status moe_fused_forward_noalloc(const moe_fused_args* args, hipStream_t str
  *   q_out, k_out   as q, k (out); may be q, k themselves, and must not
  *              overlap them otherwise
  * Supported: D % 8 == 0 and D <= 512; R even, 0 < R <= D, R % 16 == 0
- * (R % 8 == 0 when interleaved); eps >= 0 and finite; T * (NHq + NHk) < 2^32.
+ * (R % 8 == 0 when interleaved); eps >= 0 and finite; T * (NHq + NHk) < 2^32,
+ * and T times a token's waves (one for 6 * 512 / D heads of a side, D rounded up
+ * to a power of two) < 2^26.
  */
 typedef struct {
   const void* q;
@@ -446,7 +448,9 @@ moe_status moe_qk_norm_rope(const moe_qk_norm_rope_args* args, hipStream_t strea
  *             V scales [4 quads][D / 32][4 tokens]
  *           (the order in which moe_cache4_attend's matrix operands take them)
  * Supported: D 64, 128, 192 or 256; page_size a multiple of 16, at most 4096;
- * NKV <= 65535; num_pages * NKV * page_size / 16 < 2^31 tiles.
+ * NKV <= 65535; num_pages * NKV * page_size / 16 < 2^31 tiles; in one write or
+ * read T < 2^31 and ((T + 15) / 16 * h + 8) * 2 * D < 2^32, h = NKV, or NKV / 4
+ * where NKV is a multiple of 4.
  */
 typedef struct {
   void* pages;
@@ -559,7 +563,7 @@ moe_status moe_cache4_attend(const moe_cache4* cache, const moe_cache4_attend_ar
  *                 overlap, graphs included, need workspaces of their own.
  * Supported: D 64, 128, 192 or 256; NHq a multiple of NKV; scale positive and
  * finite; k and v token strides <= 2^24; Tq * NHq and Tk < 2^31 - 2^16;
- * (B + 8) * NKV < 2^29.
+ * Tq * NHq / 256 + (B + 8) * NKV < 2^23 - 8.
  */
 typedef struct {
   const void* q;

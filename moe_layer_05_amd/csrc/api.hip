@@ -114,6 +114,8 @@ moe_status guarded(F&& launch) {
 bool stride_ok(int64_t stride, int64_t heads, int64_t D) {
   return stride >= heads * D && stride % 8 == 0;
 }
+// A launch's threads are counted in 32 bits.
+bool grid_ok(int64_t workgroups, int64_t threads) { return workgroups <= 0xFFFFFFFFll / threads; }
 bool head_size_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 // Scores are compared before they are scaled, so the scale is positive.
 bool scale_ok(float s) { return s > 0.0f && s <= 3.0e38f; }
@@ -144,6 +146,8 @@ moe_status check_cache_tokens(const moe_cache4* c, const moe_cache4_tokens* t) {
   if (t->B < 0 || t->T < 0 || t->max_pages < 0 || t->table_stride < t->max_pages) return MOE_ERR_SHAPE;
   if (!t->cu_seqlens && t->T != t->B) return MOE_ERR_SHAPE;
   if (t->T >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  // 16 tokens of one kv head a workgroup, of four in large calls of NKV % 4 == 0
+  if (!grid_ok((t->T + 15) / 16 * (c->NKV % 4 ? c->NKV : c->NKV / 4) + 8, 2 * c->D)) return MOE_ERR_UNSUPPORTED;
   if (!stride_ok(t->k_token_stride, c->NKV, c->D) || !stride_ok(t->v_token_stride, c->NKV, c->D))
     return MOE_ERR_UNSUPPORTED;
   if (t->T == 0) return MOE_OK;
@@ -169,7 +173,9 @@ moe_status check_prompt_shape(int32_t B, int64_t Tq, int64_t Tk, int32_t NHq, in
   if (!head_size_ok(D)) return MOE_ERR_UNSUPPORTED;
   // rows and workgroups are counted in 32 bits
   const int64_t most = ((int64_t)1 << 31) - (1 << 16);
-  if (Tq >= most / NHq || Tk >= most || ((int64_t)B + 8) * NKV >= most / 4) return MOE_ERR_UNSUPPORTED;
+  if (Tq >= most / NHq || Tk >= most) return MOE_ERR_UNSUPPORTED;
+  // 256 rows a workgroup, and a part tile for each sequence (split keys: few rows)
+  if (!grid_ok(Tq * NHq / 256 + ((int64_t)B + 8) * NKV + 8, 512)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -691,6 +697,7 @@ moe_status moe_qk_norm_rope(const moe_qk_norm_rope_args* a, hipStream_t stream) 
             !stride_ok(a->k_out_token_stride, a->NHk, a->D)))
     return MOE_ERR_UNSUPPORTED;
   if (a->T >= ((int64_t)1 << 32) / (a->NHq + (int64_t)a->NHk)) return MOE_ERR_UNSUPPORTED;
+  if (!grid_ok(qk_norm_rope_waves(a->T, a->NHq, a->NHk, a->D) + 4, 64)) return MOE_ERR_UNSUPPORTED;
   if (a->T == 0) return MOE_OK;
   if (!a->q || !a->positions || !a->cos_sin || !a->q_out || (k && (!a->k || !a->k_out)))
     return MOE_ERR_NULL;

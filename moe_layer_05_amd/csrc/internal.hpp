@@ -154,6 +154,8 @@ struct HeadRows {
 };
 // RMS norm (where a weight is given) and rotary embedding of the query and
 // key heads; weights bfloat16, or float32 with weights_f32.
+// Waves of its largest launches.
+int64_t qk_norm_rope_waves(int64_t T, int NHq, int NHk, int D);
 hipError_t launch_qk_norm_rope(const HeadRows& q, const HeadRows& k, const int64_t* positions,
                                const float* table, int64_t max_pos, int64_t T, int D, int R,
                                bool interleaved, bool weights_f32, float eps, int num_cus,

@@ -649,9 +649,11 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
             make_float4(o[i][r], o[i][r + 1], o[i][r + 2], o[i][r + 3]);
     if (g == 0) a.part_ml[at] = make_float2(m, l);
   }
-  if (__any(odd != 0.0f) && mine > 0)
+  if (__any(odd != 0.0f) && mine > 0) {
+    wait_loads<0>();                                   // the rows' stores above come first
     mend_rows<D>(a, q0, nq, row0, min(kRows, nr - row0), kvh, k0, nk_all, key0, min(nk_all, key0 + mine * KB),
                  alone, split);
+  }
 }
 
 // Joins the splits of a row, a wave each: the block that computed it is found

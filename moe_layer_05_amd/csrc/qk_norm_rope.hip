@@ -34,6 +34,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWavesPerBlock = kThreads / kWave;
+constexpr int kMostSteps = 6;              // of a wave
+
+// Heads that a wave takes in one step: 64 lanes, D / 8 of them (rounded up to
+// a power of two) a head.
+int heads_of_step(int D) {
+  int lanes = 1;
+  while (lanes < D / 8) lanes *= 2;
+  return kWave / lanes;
+}
 
 struct HeadsArgs {
   const uint4* x;      // bf16, 8 per uint4
@@ -195,18 +204,21 @@ hipError_t prepare_qk_norm_rope_kernels() {
   return e;
 }
 
+int64_t qk_norm_rope_waves(int64_t T, int NHq, int NHk, int D) {
+  const int64_t heads = (int64_t)kMostSteps * heads_of_step(D);
+  return T * ((NHq + heads - 1) / heads + (NHk + heads - 1) / heads);
+}
+
 hipError_t launch_qk_norm_rope(const HeadRows& q, const HeadRows& k, const int64_t* positions,
                                const float* table, int64_t max_pos, int64_t T, int D, int R,
                                bool interleaved, bool weights_f32, float eps, int num_cus,
                                hipStream_t stream) {
   NormRopeArgs a{};
-  int g = 0;
-  while ((1 << g) < D / 8) ++g;
-  const int step = kWave >> g;
-  // Steps per wave: as many as leave every SIMD four waves, at most 6.
+  const int step = heads_of_step(D), g = 6 - __builtin_ctz(step);
+  // Steps per wave: as many as leave every SIMD four waves, at most kMostSteps.
   const int64_t steps = T * ((q.heads + step - 1) / step + (k.heads + step - 1) / step);
   int64_t iters = steps / ((int64_t)num_cus * 16);
-  iters = iters < 1 ? 1 : (iters > 6 ? 6 : iters);
+  iters = iters < 1 ? 1 : (iters > kMostSteps ? kMostSteps : iters);
   const HeadRows* src[2] = {&q, &k};
   for (int i = 0; i < 2; ++i) {
     HeadsArgs& s = a.side[i];

@@ -147,6 +147,24 @@ def test_prompt_workspace(L):
     assert need(2, 9, 4096, 3, 2, 128) == 0 and need(-1, 9, 4096, 4, 2, 128) == 0
 
 
+def test_launches_of_more_than_32_bits(L):
+    """The largest calls that a launch's 32-bit count of threads holds pass the
+    shape checks (and are refused for their null pointer), one more is
+    refused."""
+    big = dict(NHk=0, k=0, ko=0, kw=0, ks=0, kos=0)
+    assert norm_rope(L, T=(1 << 26) - 5, q=0, **big) == NULL
+    assert norm_rope(L, T=(1 << 26) - 4, **big) == UNSUP
+    most = 16 * (0xFFFFFFFF // 256 - 8)                    # 256 threads for 16 tokens of a head
+    for fn in (L.moe_cache4_write, L.moe_cache4_read):
+        assert places(fn, cache(heads=1), T=most, k=0, ks=128, vs=128) == NULL
+        assert places(fn, cache(heads=1), T=most + 1, ks=128, vs=128) == UNSUP
+        assert places(fn, cache(heads=4), T=most, k=0, ks=512, vs=512) == NULL
+        assert places(fn, cache(heads=4), T=most + 1, ks=512, vs=512) == UNSUP
+    room = (1 << 23) - 9                                   # workgroups of 512 threads
+    assert prompt(L, B=room // 2 - 8, q=0) == NULL
+    assert prompt(L, B=room // 2 - 7) == UNSUP
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     i32 = torch.zeros(3, dtype=torch.int32)
