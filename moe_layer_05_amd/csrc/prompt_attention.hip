@@ -28,17 +28,21 @@
 // two), so most tiles skip the rescaling of O^T.
 //
 // Work split: a workgroup of eight waves takes 256 rows, 32 a wave, of one kv
-// head (of four waves 128, where that gives all compute units work); a row is (query, head of the group), so that the heads of a group share
+// head; a row is (query, head of the group), so that the heads of a group share
 // their keys and short prompts fill the rows.  K and V tiles of 64 keys (32 for
 // D = 192, 256) come to LDS by direct loads into a ring of four, two tiles
 // ahead; rows behind the last key repeat it.  The two waves of a SIMD work in
 // opposite phases (below): a tile's two products are 32 matrix instructions
 // (D = 128), its softmax about 110 vector instructions of which 32 are
-// exponentials, so neither may wait for the other.  Few query tiles over many keys split the keys; the parts go
-// to scratch in float32 and a second launch joins them.
+// exponentials, so neither may wait for the other.  Few rows take workgroups of
+// 128 or 64 rows, in which two waves share 32 rows and take half of each tile's
+// keys each; their sums meet in the LDS at the end (launch_head has the
+// measurements).  Few query tiles over many keys split the keys over
+// workgroups; the parts go to scratch in float32 and a second launch joins them
+// (prompt_splits).
 //
-// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 517 us = 1.06
-// PFLOP/s (D = 64, 192, 256: 0.79, 1.10, 1.11; not causal, D = 128: 1.15); a
+// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 502 us = 1.10
+// PFLOP/s (D = 64, 192, 256: 0.92, 1.10, 1.11; not causal, D = 128: 1.15); a
 // library product of 8192^3 reaches 1.38 on the same card.  In parts (not
 // causal, D = 128, before the values were read ahead: 975 us): without the
 // loads to LDS 905, without the softmax as well 858, without the LDS reads as
@@ -52,6 +56,7 @@
 // pairs are replaced, and a wave that ends with a value that is not finite
 // looks for values among its masked pairs that 0 * NaN carried over
 // (mend_rows).
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -63,7 +68,6 @@ namespace {
 constexpr int kRows = 32;                       // rows of a wave
 constexpr int kMaxSplits = 64;
 constexpr int kLeast = 4;                       // tiles of keys of a split, at least
-constexpr int kWorth = 18;                      // tiles of keys from which splits are made
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
@@ -74,14 +78,17 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 #define MOE_LDS __attribute__((address_space(3)))
 
 // Shape of a kernel: head size, waves of a workgroup, buffers of the ring.
-template <int D_, int WAVES_, int BUFS_>
+template <int D_, int WAVES_, int BUFS_, int PARTS_ = 1>
 struct Shape {
   static constexpr int D = D_, kWaves = WAVES_, kBufs = BUFS_;
   static constexpr int kThreads = kWaves * kWave;
-  static constexpr int kBlockRows = kWaves * kRows;
+  static constexpr int kParts = PARTS_;                   // waves that share 32 rows, and a tile's keys
+  static constexpr int kGroups = kWaves / kParts;         // of 32 rows
+  static constexpr int kBlockRows = kGroups * kRows;
   static constexpr bool kPaired = kWaves == 8;            // two waves on a SIMD, in opposite phases
   // keys of a tile
   static constexpr int KB = D <= 128 ? 64 : 32;
+  static constexpr int KW = KB / kParts;                  // of them a wave's
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kHalf = KB * kRowBytes;            // K (or V) of a tile
   static constexpr int kLoads = 2 * kHalf / 1024 / kWaves;  // 1 KB loads of a wave per tile
@@ -93,7 +100,7 @@ struct Shape {
   static constexpr int kReadAhead = D == 128 || D == 192 ? 4 : 2;
   static constexpr bool kTurns = D <= 192;
   // value operands read during the softmax
-  static constexpr int kPre = D == 128 ? 8 : (D == 192 ? 2 : 0);
+  static constexpr int kPre = D == 128 ? 8 / kParts : (D == 192 ? 2 : 0);
   // D = 64: two workgroups to a compute unit
   static constexpr int kWavesPerSimd = D == 64 && kPaired ? 4 : 2;
   // The 16-byte pieces of a row are XOR-ed with a function of the row inside
@@ -236,7 +243,7 @@ __attribute__((noinline)) __device__ void mend_rows(PromptArgs a, int q0, int nq
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attention_kernel(
     PromptArgs a, int slots) {
-  constexpr int D = S::D, KB = S::KB;
+  constexpr int D = S::D, KB = S::KB, KW = S::KW;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
@@ -312,7 +319,8 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   nk_all = __builtin_amdgcn_readfirstlane(nk_all);
   const int nr = nq * G;                              // rows: (query, head of the group)
   const int block0 = tile * S::kBlockRows;
-  const int row0 = block0 + wave * kRows;
+  const int part = wave / S::kGroups;                 // of a tile's keys
+  const int row0 = block0 + wave % S::kGroups * kRows;
   const int last_row = min(block0 + S::kBlockRows, nr) - 1;
   // this split's tiles of keys; from here on keys and limits count from its
   // first key on
@@ -398,22 +406,22 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   // leaves constants in st and d, since rows differ by multiples of 32 or 16,
   // and 8 rows further on the XOR-ed function differs in bit 1.
   const int vr = 4 * g + ((lane & 15) >> 2);
-  const uint32_t kat = lds0 + S::at(c, g);
-  const uint32_t vat = lds0 + S::kHalf + S::at(vr, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + (lane & 1) * 8;
+  const uint32_t kat = lds0 + part * (KW * S::kRowBytes) + S::at(c, g);
+  const uint32_t vat = lds0 + S::kHalf + part * (KW * S::kRowBytes) + S::at(vr, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + (lane & 1) * 8;
 
   // Tiles that every row of the workgroup sees whole, and this wave's tiles.
   const int whole = limit(block0) / KB;
   const int mine = (wave_max + KB - 1) / KB;
   float m, l;
-  v16f o[D / 32], s[KB / 32];
-  v8bf pb[KB / 16];
+  v16f o[D / 32], s[KW / 32];
+  v8bf pb[KW / 16];
 
   // Operands of the matrix instructions.  Scores of tile t: instruction n
   // takes K rows 32 i .. of step st; values: V^T rows 32 d .. of 16 keys u.
   // Neighbours add to different accumulators where there are several.
-  constexpr int kOps = (D / 16) * (KB / 32);           // of either product
+  constexpr int kOps = (D / 16) * (KW / 32);           // of either product
   auto key_operand = [&](uint32_t kt, int n) {
-    const int st = n / (KB / 32), i = n % (KB / 32);
+    const int st = n / (KW / 32), i = n % (KW / 32);
     const uint32_t at = (kt ^ (32 * (st % (S::kGroup / 2)))) + (2 * st / S::kGroup) * (S::kGroup * 16);
     return *(const MOE_LDS v8bf*)(uintptr_t)(at + i * 32 * S::kRowBytes);
   };
@@ -430,7 +438,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   };
   // S^T of tile t, and O^T += V^T P^T of tile t - 1 with P as the last softmax
   // left it, each on request.  Together: where two score accumulators take
-  // turns (KB = 64), a quarter of the values, then two scores and a value at a
+  // turns (KW = 64), a quarter of the values, then two scores and a value at a
   // time, then the last values; with one, values and scores in turn (kTurns).
   // So no instruction waits for the one before it, the first ones find their
   // operands in registers (ahead, read during the softmax, when the LDS has
@@ -451,7 +459,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
       if (!kV) return 2 * n;
       if (!kS) return 2 * n + 1;
       if (!S::kTurns) return n < kOps ? 2 * n : 2 * (n - kOps) + 1;
-      if (KB == 32) return n % 2 ? n - 1 : n + 1;
+      if (KW == 32) return n % 2 ? n - 1 : n + 1;
       constexpr int kQ = kOps / 4;
       if (n < kQ) return 2 * n + 1;
       if (n >= kAll - kQ) return 2 * (n - kOps) + 1;
@@ -475,7 +483,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     };
     if constexpr (kS) {
 #pragma unroll
-      for (int i = 0; i < KB / 32; ++i)
+      for (int i = 0; i < KW / 32; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[i][r] = 0.0f;
     }
@@ -487,8 +495,8 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
       for (int i = 0; i < kAt; ++i) {
         const int op = at(n + i) / 2;
         if (at(n + i) % 2 == 0) {
-          const int j = op % (KB / 32);
-          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[(n / kAt) & 1][i], q[op / (KB / 32)], s[j], 0, 0, 0);
+          const int j = op % (KW / 32);
+          s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[(n / kAt) & 1][i], q[op / (KW / 32)], s[j], 0, 0, 0);
         } else {
           const int d = op % (D / 32);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op < S::kPre ? ahead[op < S::kPre ? op : 0] : f[(n / kAt) & 1][i],
@@ -502,16 +510,16 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   // P of S^T, with the running maximum and sum.
   auto softmax = [&](int t) {
     if (t >= whole) {                                  // uniform
-      const int left = lim - t * KB - 4 * g;           // of this lane's keys, from register 0's on
+      const int left = lim - t * KB - part * KW - 4 * g;           // of this lane's keys, from register 0's on
 #pragma unroll
-      for (int i = 0; i < KB / 32; ++i)
+      for (int i = 0; i < KW / 32; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           s[i][r] = i * 32 + 8 * (r >> 2) + (r & 3) < left ? s[i][r] : kNegInf;
     }
     float top = s[0][0];
 #pragma unroll
-    for (int i = 0; i < KB / 32; ++i)
+    for (int i = 0; i < KW / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[i][r]);
     top *= scale2;
@@ -529,7 +537,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     const float base = m == kNegInf ? 0.0f : -m;
     float sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < KB / 16; ++u) {
+    for (int u = 0; u < KW / 16; ++u) {
       uint32_t pw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -545,7 +553,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
     // P is made here and not, as the compiler would have it, where the next
     // phase's products first need it
 #pragma unroll
-    for (int u = 0; u < KB / 16; ++u) asm volatile("" : "+v"(pb[u]));
+    for (int u = 0; u < KW / 16; ++u) asm volatile("" : "+v"(pb[u]));
     asm volatile("" : "+v"(l));
   };
 
@@ -605,12 +613,38 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   }
   if (S::kPaired && !late) barrier();                  // the second half's last products
 
+  l += __shfl_xor(l, 32);
+  if constexpr (S::kParts == 2) {
+    // The second parts' sums go to the first through the LDS, register by
+    // register, when its last reader is done.
+    barrier();
+    float* box = reinterpret_cast<float*>(smem) + wave % S::kGroups * (kRows * D + 2 * kWave) + lane;
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) box[(i * 16 + r) * kWave] = o[i][r];
+      box[kRows * D] = m;
+      box[kRows * D + kWave] = l;
+    }
+    barrier();
+    if (part) return;
+    const float m2 = box[kRows * D], l2 = box[kRows * D + kWave], top = fmaxf(m, m2);
+    // as the join of splits has it
+    const float f = m == kNegInf ? l : __builtin_amdgcn_exp2f(m - top);
+    const float f2 = m2 == kNegInf ? l2 : __builtin_amdgcn_exp2f(m2 - top);
+    m = top;
+    l = f * l + f2 * l2;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] = f * o[i][r] + f2 * box[(i * 16 + r) * kWave];
+  }
   float odd = 0.0f;                                    // NaN as soon as one value is not finite
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) odd = fmaf(o[i][r], 0.0f, odd);
-  l += __shfl_xor(l, 32);
   int end_c = c;
   asm volatile("" : "+v"(end_c));                      // worked out again: registers of the loop
   const int row = row0 + end_c;
@@ -724,38 +758,53 @@ void launch_one(const PromptArgs& p, hipStream_t stream) {
       p, (int)slots);
 }
 
+// Workgroups of 256, 128 and 64 rows.
 template <int D>
-using Pairs = Shape<D, 8, 4>;                          // 256 rows
+using Rows256 = Shape<D, 8, 4>;
 template <int D>
-using Fours = Shape<D, 4, 4>;                          // 128 rows
+using Rows128 = Shape<D, D == 192 ? 4 : 8, 4, D == 192 ? 1 : 2>;
+template <int D>
+using Rows64 = Shape<D, 4, 4, 2>;
 
+template <typename S>
+hipError_t prepare_one() {
+  return prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<S>), S::kLds);
+}
 template <int D>
 hipError_t prepare_head() {
-  hipError_t e = prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<Pairs<D>>), Pairs<D>::kLds);
-  if (e == hipSuccess) e = prepare_kernel(reinterpret_cast<const void*>(&prompt_join_kernel<Pairs<D>>), 0);
-  if constexpr (D < 256)
-    if (e == hipSuccess)
-      e = prepare_kernel(reinterpret_cast<const void*>(&prompt_attention_kernel<Fours<D>>), Fours<D>::kLds);
+  hipError_t e = prepare_one<Rows256<D>>();
+  if (e == hipSuccess) e = prepare_kernel(reinterpret_cast<const void*>(&prompt_join_kernel<Rows256<D>>), 0);
+  if constexpr (D < 256) {
+    if (e == hipSuccess) e = prepare_one<Rows128<D>>();
+  }
+  if constexpr (D <= 128) {
+    if (e == hipSuccess) e = prepare_one<Rows64<D>>();
+  }
   return e;
 }
 
-// Workgroups of four waves where the keys are whole and the rows leave them in
-// one round of 256 compute units (two each at D = 64): a compute unit then has
-// less of them, and a wave that has its SIMD to itself goes through a tile
-// without waiting for the other's phase.  Four against eight waves: 100 tokens,
-// 16 heads over 2 of 128, 8.7 and 11.2 us; 1024 tokens, 16 over 4, 27.3 and 31.4
-// us; 2048 tokens 49.1 and 56.1 us, D = 64 31.1 and 38.7 us; where they do not
-// fit one round, 8 x 1024 tokens, 81 and 68 us (D = 64 the same).  Not at D =
-// 256: 1024 tokens, 8 heads over 2, 41 and 37 us (it spills).
+// Where the keys are not split, the fewest rows a workgroup that leave the rows
+// in one round of the 256 compute units (two workgroups each at D = 64): the
+// waves that the rows do not need share a tile's keys, so that the chain of
+// tiles, which is the time then, has shorter links.  256, 128 and 64 rows, one
+// sequence, 16 heads over 4 of 128: 512 tokens 20.0, 16.2, 13.6 us; 1024 tokens
+// 31.8, 24.5, 21.7 us; 2048 tokens, where 64 rows take two rounds, 55.7, 41.2,
+// 45.1 us; 8 x 1024 tokens (two rounds of 128) 65.9, 75.6, 106 us; D = 64, 2048
+// tokens 38.6, 28.6, 24.6 us.  D = 192 has tiles of 32 keys, which do not divide
+// (256 tokens, 256 and 128 rows: 18.2, 13.6 us), and 128 rows of D = 256 spill
+// (1024 tokens: 37 and 41 us).
 template <int D>
 void launch_head(const PromptArgs& p, hipStream_t stream) {
-  if constexpr (D < 256) {
-    if (p.splits == 1 && p.Tq * p.NHq <= (D == 64 ? 512 : 256) * Fours<D>::kBlockRows)
-      return launch_one<Fours<D>>(p, stream);
+  const int64_t round = D == 64 ? 512 : 256, rows = p.Tq * p.NHq;
+  if constexpr (D <= 128) {
+    if (p.splits == 1 && rows <= round * Rows64<D>::kBlockRows) return launch_one<Rows64<D>>(p, stream);
   }
-  launch_one<Pairs<D>>(p, stream);
+  if constexpr (D < 256) {
+    if (p.splits == 1 && rows <= round * Rows128<D>::kBlockRows) return launch_one<Rows128<D>>(p, stream);
+  }
+  launch_one<Rows256<D>>(p, stream);
   if (p.splits > 1)
-    prompt_join_kernel<Pairs<D>><<<dim3((unsigned)((p.Tq * p.NHq + 3) / 4)), dim3(256), 0, stream>>>(p);
+    prompt_join_kernel<Rows256<D>><<<dim3((unsigned)((p.Tq * p.NHq + 3) / 4)), dim3(256), 0, stream>>>(p);
 }
 
 }  // namespace
@@ -768,20 +817,33 @@ hipError_t prepare_prompt_kernels() {
   return e;
 }
 
-// Splits of the keys where the query tiles leave most of the 256 compute
-// units without work: as many as fill them, each with kLeast tiles if a
-// sequence had all the keys.  Below kWorth tiles of keys the second launch and
-// the float32 sums cost what the shorter chains give (one sequence, 16 heads
-// over 4 of 128: 512 tokens 16.3 us whole, 22.4 us split; 256 queries over 4096
-// keys 97 us whole, 30 us split).
+// Splits of the keys, where 256 rows a workgroup leave compute units without
+// work: as many as fill them, each with kLeast tiles if a sequence had all the
+// keys, and as the estimate of the time takes least, in us: a tile of a
+// workgroup of 256 rows, a second launch, and the parts' way to memory and back
+// at 4.5 TB/s.  None where the tiles of the workgroup of fewest rows, one after
+// the other, take less than that.  Measured, whole and split, us: 1 query over
+// 4096 keys, 16 heads over 2 of 128, 60.2 and 13.5; 256 queries over 4096 keys,
+// 16 over 4, 62.3 and 30.1; 1024 over 8192, 8 over 1, 120 and 57; 2048 over 2048,
+// 8 over 1, 35.2 and 41.2; 700 over 1500, 16 over 2, 27.9 and 32.4.
 int prompt_splits(int64_t Tq, int64_t Tk, int64_t B, int NHq, int NKV, int D) {
   if (B == 0 || Tq == 0) return 1;
-  const int64_t units = prompt_slots(Tq, B, NHq / NKV, Pairs<64>::kBlockRows) * NKV;
+  const int64_t units = prompt_slots(Tq, B, NHq / NKV, Rows256<64>::kBlockRows) * NKV;
   const int64_t tiles = Tk / (D <= 128 ? 64 : 32);
-  const int64_t most = tiles < kWorth ? 1 : tiles / kLeast;
-  int64_t s = 256 / units;
-  if (s > most) s = most;
-  return (int)(s < 2 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
+  const int64_t most = std::min<int64_t>(std::min(256 / units, tiles / kLeast), kMaxSplits);
+  const double whole = D == 64 ? 0.54 : (D == 128 ? 0.88 : (D == 192 ? 0.86 : 1.58));   // us a tile
+  const double tile = D == 64 ? 1.0 : (D == 128 ? 1.5 : (D == 192 ? 1.16 : 1.58));
+  const double part = (double)Tq * NHq * D * 8 / 4.5e6, launch = 6.0;
+  double best = (double)tiles * whole;
+  int splits = 1;
+  for (int s = 2; s <= most; ++s) {
+    const double us = tiles * tile / s + launch + s * part;
+    if (us < best) {
+      best = us;
+      splits = s;
+    }
+  }
+  return splits;
 }
 
 size_t prompt_workspace(int64_t Tq, int NHq, int D, int splits) {

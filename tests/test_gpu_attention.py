@@ -459,10 +459,8 @@ def test_prompt_groups_and_splits(D, NHq, NKV, nq, nk, causal):
 @pytest.mark.parametrize("D,NHq,NKV", [(64, 4, 2), (128, 2, 1), (128, 8, 1), (192, 4, 2), (256, 2, 2)])
 def test_prompt_few_and_many_rows(D, NHq, NKV, causal):
     """Few rows and many (of padding behind the last sequence) take workgroups
-    of different sizes, NaN and infinity in masked and seen places included.
-    A row's sums have the same order in both, so every bit is the same; but for
-    D > 128, whose tiles of 32 keys are so many (1028 / 32) that the few rows'
-    keys are split: there both are held to the oracle, and NaN to its places."""
+    of different sizes, in some of which waves share a tile's keys: all are held
+    to the oracle, and NaN and infinity, in masked and seen places, to theirs."""
     say("prompt rows", D, NHq, NKV, causal)
     g = gen(D + NHq)
     nq, nk = [300, 0, 33, 1, 129, 70], [300, 9, 500, 70, 129, 20]
@@ -472,22 +470,22 @@ def test_prompt_few_and_many_rows(D, NHq, NKV, causal):
     v[299, 0, 5] = float("nan")                # seen by the first sequence's last query
     k[280, 0, 7] = float("inf")
     q[320, 0, 3] = float("nan")
-    pad, n = 80000 // NHq, sum(nq)
+    n = sum(nq)
     same = lambda a, b: bool(((a == b) | (a.isnan() & b.isnan())).all())  # noqa: E731
     for c, (x, y, z) in enumerate((clean, (q, k, v))):
         args = y.to(DEV), z.to(DEV), i32(cu(nq)), i32(cu(nk))
         few, lse = mm.prompt_attention(x.to(DEV), *args, causal=causal, return_lse=True)
-        many, lse2 = mm.prompt_attention(torch.cat([x, torch.full((pad, NHq, D), float("nan"), dtype=x.dtype)]).to(DEV),
-                                         *args, causal=causal, return_lse=True)
         if c == 0:
             check_prompt(few, lse, x, y, z, nq, nk, causal, D ** -0.5)
-            check_prompt(many[:n], lse2[:n], x, y, z, nq, nk, causal, D ** -0.5)
         else:
             assert few[299, 0].isnan().any() and few[320, 0].isnan().all()
-        assert same(few.isnan(), many[:n].isnan()) and same(lse.isnan(), lse2[:n].isnan())
-        if D <= 128:
-            assert same(few, many[:n]) and same(lse, lse2[:n])
-        assert not many[n:].any() and torch.isneginf(lse2[n:]).all()
+        for rows in (20000, 40000, 80000, 160000):
+            pad = torch.full((rows // NHq - n, NHq, D), float("nan"), dtype=x.dtype)
+            many, lse2 = mm.prompt_attention(torch.cat([x, pad]).to(DEV), *args, causal=causal, return_lse=True)
+            if c == 0:
+                check_prompt(many[:n], lse2[:n], x, y, z, nq, nk, causal, D ** -0.5)
+            assert same(few.isnan(), many[:n].isnan()) and same(lse.isnan(), lse2[:n].isnan())
+            assert not many[n:].any() and torch.isneginf(lse2[n:]).all()
 
 
 def test_prompt_splits_non_finite():
