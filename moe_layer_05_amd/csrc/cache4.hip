@@ -4,9 +4,10 @@
 // A workgroup takes 16 consecutive packed tokens of one or four kv heads:
 // 16 * D / 8 threads, each 8 features of one token's key and value (one
 // 16-byte load or store each, one word of codes each); four neighbouring lanes
-// share a group of 32 and find its largest magnitude by two lane swaps.  Each thread finds
-// its token's sequence by a binary search of cu_seqlens and its page in the
-// block table, so ragged batches need no plan made on the host.  A place is
+// share a group of 32 and find its largest magnitude by two lane swaps.  Each
+// thread finds its token's sequence by a binary search of cu_seqlens and its
+// page in the block table, so ragged batches need no plan made on the host.  A
+// place is
 // used only if its position is not negative, lies in the table's columns and
 // its page id names a page of the cache: other tokens are skipped by a write
 // and read as zeros, and no address is formed from them.

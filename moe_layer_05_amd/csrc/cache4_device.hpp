@@ -7,8 +7,9 @@
 // magnitude to at most 7: 7 rounds to 6, the largest code, and nothing is off
 // by more than half a step of the grid's top interval; over normal values
 // the mean squared error is 6% below that of the largest code's own binade
-// (amax < 8, which clips 7..8 to 6) and that of never exceeding 6.  A value read back is exact in bfloat16.  A group with an
-// infinity or a NaN gets the byte 255 and reads back as NaN.
+// (amax < 8, which clips 7..8 to 6) and that of never exceeding 6.  A value
+// read back is exact in bfloat16.  A group with an infinity or a NaN gets the
+// byte 255 and reads back as NaN.
 //
 // [page][kv head][tile of 16 tokens], a tile of 17 * D bytes:
 //   K codes  [16 tokens][D / 2], feature 2i in the low half of byte i

@@ -23,9 +23,8 @@
 // relative each, random over the keys: the output's error stays at the size of
 // its own rounding; a second bfloat16 for the rest, as the cache's attention
 // has it, would add half as many matrix instructions); their sum is taken in
-// float32 before that.  The running
-// maximum moves only when a score passes it by more than 8 (in powers of
-// two), so most tiles skip the rescaling of O^T.
+// float32 before that.  The running maximum moves only when a score passes it by
+// more than 8 (in powers of two), so most tiles skip the rescaling of O^T.
 //
 // Work split: a workgroup of eight waves takes 256 rows, 32 a wave, of one kv
 // head; a row is (query, head of the group), so that the heads of a group share
@@ -407,7 +406,8 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void prompt_attentio
   // and 8 rows further on the XOR-ed function differs in bit 1.
   const int vr = 4 * g + ((lane & 15) >> 2);
   const uint32_t kat = lds0 + part * (KW * S::kRowBytes) + S::at(c, g);
-  const uint32_t vat = lds0 + S::kHalf + part * (KW * S::kRowBytes) + S::at(vr, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + (lane & 1) * 8;
+  const uint32_t vat = lds0 + S::kHalf + part * (KW * S::kRowBytes) +
+                       S::at(vr, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + (lane & 1) * 8;
 
   // Tiles that every row of the workgroup sees whole, and this wave's tiles.
   const int whole = limit(block0) / KB;
