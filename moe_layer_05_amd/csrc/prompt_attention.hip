@@ -38,7 +38,8 @@
 // keys each; their sums meet in the LDS at the end (launch_head has the
 // measurements).  Few query tiles over many keys split the keys over
 // workgroups; the parts go to scratch in float32 and a second launch joins them
-// (prompt_splits).
+// (prompt_splits).  Many rows of short sequences take tiles of 32 keys, with
+// more workgroups on a compute unit.
 //
 // Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 502 us = 1.10
 // PFLOP/s (D = 64, 192, 256: 0.92, 1.10, 1.11; not causal, D = 128: 1.15); a
@@ -77,7 +78,7 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 #define MOE_LDS __attribute__((address_space(3)))
 
 // Shape of a kernel: head size, waves of a workgroup, buffers of the ring.
-template <int D_, int WAVES_, int BUFS_, int PARTS_ = 1>
+template <int D_, int WAVES_, int BUFS_, int PARTS_ = 1, int KB_ = D_ <= 128 ? 64 : 32>
 struct Shape {
   static constexpr int D = D_, kWaves = WAVES_, kBufs = BUFS_;
   static constexpr int kThreads = kWaves * kWave;
@@ -86,7 +87,7 @@ struct Shape {
   static constexpr int kBlockRows = kGroups * kRows;
   static constexpr bool kPaired = kWaves == 8;            // two waves on a SIMD, in opposite phases
   // keys of a tile
-  static constexpr int KB = D <= 128 ? 64 : 32;
+  static constexpr int KB = KB_;
   static constexpr int KW = KB / kParts;                  // of them a wave's
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kHalf = KB * kRowBytes;            // K (or V) of a tile
@@ -99,7 +100,7 @@ struct Shape {
   static constexpr int kReadAhead = D == 128 || D == 192 ? 4 : 2;
   static constexpr bool kTurns = D <= 192;
   // value operands read during the softmax
-  static constexpr int kPre = D == 128 ? 8 / kParts : (D == 192 ? 2 : 0);
+  static constexpr int kPre = D == 128 ? KW / 8 : (D == 192 ? 2 : 0);
   // D = 64: two workgroups to a compute unit
   static constexpr int kWavesPerSimd = D == 64 && kPaired ? 4 : 2;
   // The 16-byte pieces of a row are XOR-ed with a function of the row inside
@@ -765,6 +766,10 @@ template <int D>
 using Rows128 = Shape<D, D == 192 ? 4 : 8, 4, D == 192 ? 1 : 2>;
 template <int D>
 using Rows64 = Shape<D, 4, 4, 2>;
+// 128 rows, with tiles of 32 keys: two workgroups on a compute unit (four at D
+// = 64), so that the beginning and end of one run beside the others' products.
+template <int D>
+using Short128 = Shape<D, 4, 4, 1, 32>;
 
 template <typename S>
 hipError_t prepare_one() {
@@ -779,6 +784,7 @@ hipError_t prepare_head() {
   }
   if constexpr (D <= 128) {
     if (e == hipSuccess) e = prepare_one<Rows64<D>>();
+    if (e == hipSuccess) e = prepare_one<Short128<D>>();
   }
   return e;
 }
@@ -793,6 +799,14 @@ hipError_t prepare_head() {
 // tokens 38.6, 28.6, 24.6 us.  D = 192 has tiles of 32 keys, which do not divide
 // (256 tokens, 256 and 128 rows: 18.2, 13.6 us), and 128 rows of D = 256 spill
 // (1024 tokens: 37 and 41 us).
+//
+// More rows whose sequences have few keys (8 D on average; at D = 64 also where
+// they take less than a second round) do not lose to the smaller tiles what they
+// win at their beginnings and ends.  Short128 against 256 rows, 32 heads over 8
+// of 128: 64 x 128 tokens 42 and 59 us, 32 x 256 51 and 66 us; 16 over 4: 16 x
+// 1024 tokens 108 and 114 us, 3 x 1500 48 and 45 us, 8192 tokens 555 and 510 us;
+// D = 64: 6 x 1024 tokens 33 and 37 us, 32 x 256 28 and 31 us, 8 x 1024 45 and
+// 42 us.
 template <int D>
 void launch_head(const PromptArgs& p, hipStream_t stream) {
   const int64_t round = D == 64 ? 512 : 256, rows = p.Tq * p.NHq;
@@ -801,6 +815,10 @@ void launch_head(const PromptArgs& p, hipStream_t stream) {
   }
   if constexpr (D < 256) {
     if (p.splits == 1 && rows <= round * Rows128<D>::kBlockRows) return launch_one<Rows128<D>>(p, stream);
+  }
+  if constexpr (D <= 128) {
+    const bool few_keys = p.Tk <= (int64_t)p.B * 8 * D || (D == 64 && rows < 2 * round * Short128<D>::kBlockRows);
+    if (p.splits == 1 && few_keys) return launch_one<Short128<D>>(p, stream);
   }
   launch_one<Rows256<D>>(p, stream);
   if (p.splits > 1)

@@ -458,9 +458,10 @@ def test_prompt_groups_and_splits(D, NHq, NKV, nq, nk, causal):
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("D,NHq,NKV", [(64, 4, 2), (128, 2, 1), (128, 8, 1), (192, 4, 2), (256, 2, 2)])
 def test_prompt_few_and_many_rows(D, NHq, NKV, causal):
-    """Few rows and many (of padding behind the last sequence) take workgroups
-    of different sizes, in some of which waves share a tile's keys: all are held
-    to the oracle, and NaN and infinity, in masked and seen places, to theirs."""
+    """Few rows and keys and many (of padding behind the last sequence) take
+    workgroups of different sizes and tiles, and in some of them waves share a
+    tile's keys: all are held to the oracle, and NaN and infinity, in masked and
+    seen places, to theirs."""
     say("prompt rows", D, NHq, NKV, causal)
     g = gen(D + NHq)
     nq, nk = [300, 0, 33, 1, 129, 70], [300, 9, 500, 70, 129, 20]
@@ -473,15 +474,16 @@ def test_prompt_few_and_many_rows(D, NHq, NKV, causal):
     n = sum(nq)
     same = lambda a, b: bool(((a == b) | (a.isnan() & b.isnan())).all())  # noqa: E731
     for c, (x, y, z) in enumerate((clean, (q, k, v))):
-        args = y.to(DEV), z.to(DEV), i32(cu(nq)), i32(cu(nk))
-        few, lse = mm.prompt_attention(x.to(DEV), *args, causal=causal, return_lse=True)
+        cus = i32(cu(nq)), i32(cu(nk))
+        few, lse = mm.prompt_attention(x.to(DEV), y.to(DEV), z.to(DEV), *cus, causal=causal, return_lse=True)
         if c == 0:
             check_prompt(few, lse, x, y, z, nq, nk, causal, D ** -0.5)
         else:
             assert few[299, 0].isnan().any() and few[320, 0].isnan().all()
-        for rows in (20000, 40000, 80000, 160000):
-            pad = torch.full((rows // NHq - n, NHq, D), float("nan"), dtype=x.dtype)
-            many, lse2 = mm.prompt_attention(torch.cat([x, pad]).to(DEV), *args, causal=causal, return_lse=True)
+        pad = lambda t, rows: torch.cat([t, torch.full((rows, *t.shape[1:]), float("nan"), dtype=t.dtype)]).to(DEV)  # noqa: E731
+        for rows, keys in ((20000, 0), (40000, 0), (40000, 9000), (80000, 0), (80000, 9000), (160000, 9000)):
+            many, lse2 = mm.prompt_attention(pad(x, rows // NHq - n), pad(y, keys), pad(z, keys), *cus,
+                                             causal=causal, return_lse=True)
             if c == 0:
                 check_prompt(many[:n], lse2[:n], x, y, z, nq, nk, causal, D ** -0.5)
             assert same(few.isnan(), many[:n].isnan()) and same(lse.isnan(), lse2[:n].isnan())
