@@ -41,7 +41,7 @@
 // (prompt_splits).  Many rows of short sequences take tiles of 32 keys, with
 // more workgroups on a compute unit.
 //
-// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 502 us = 1.10
+// Measured: 8192 tokens, 32 heads over 4 of D = 128, causal, 510 us = 1.08
 // PFLOP/s (D = 64, 192, 256: 0.92, 1.10, 1.11; not causal, D = 128: 1.15); a
 // library product of 8192^3 reaches 1.38 on the same card.  In parts (not
 // causal, D = 128, before the values were read ahead: 975 us): without the
